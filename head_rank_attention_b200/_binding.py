@@ -20,14 +20,17 @@ HRA_ERR_DEVICE_TIMEOUT = -5
 HRA_BF16 = 0
 HRA_F32 = 1
 HRA_INT8 = 2
+HRA_E4M3 = 3
+HRA_ERR_PLAN = -6
 
 STATUS_NAMES = {0: "HRA_OK", -1: "HRA_ERR_INVALID_ARG", -2: "HRA_ERR_UNSUPPORTED", -3: "HRA_ERR_WORKSPACE",
-                -4: "HRA_ERR_CUDA", -5: "HRA_ERR_DEVICE_TIMEOUT"}
+                -4: "HRA_ERR_CUDA", -5: "HRA_ERR_DEVICE_TIMEOUT", -6: "HRA_ERR_PLAN"}
 
 # Symbols declared in include/hra.h.
 EXPORTS = ("hra_workspace_size", "mlra_decode", "mla_decode", "mlra_decode_static", "hra_check_device_status",
            "hra_selftest_wait_timeout", "hra_last_error", "hra_version", "hra_prefill_workspace_size", "mlra_prefill",
-           "hra_check_prefill_status", "hra_combine_partials")
+           "hra_check_prefill_status", "hra_combine_partials", "hra_page_plan", "hra_check_plan_status",
+           "hra_cache_append", "hra_cache_load")
 
 
 class HraError(RuntimeError):
@@ -55,6 +58,7 @@ class HraDecodeParams(ctypes.Structure):
         ("out_accumulate", ctypes.c_int), ("n_out_peers", ctypes.c_int), ("out_peers", ctypes.c_void_p),
         ("cache_dtype", ctypes.c_int), ("ckv_scale", ctypes.c_void_p), ("ckv_scale_stride", ctypes.c_int64),
         ("q_positions", ctypes.c_void_p), ("part_o", ctypes.c_void_p), ("part_lse", ctypes.c_void_p),
+        ("scale_block", ctypes.c_int),
     ]
 
 
@@ -72,6 +76,45 @@ class HraPrefillParams(ctypes.Structure):
         ("out", ctypes.c_void_p), ("out_dtype", ctypes.c_int),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
         ("wait_limit", ctypes.c_int),
+    ]
+
+
+class HraPlanParams(ctypes.Structure):
+    """Mirror of hra_plan_params (field order and C types as in include/hra.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int), ("page_size", ctypes.c_int), ("max_pages", ctypes.c_int),
+        ("num_pages", ctypes.c_int), ("max_tokens", ctypes.c_int),
+        ("seq_lens", ctypes.c_void_p), ("new_tokens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("free_pages", ctypes.c_void_p), ("free_range", ctypes.c_void_p), ("seq_lens_out", ctypes.c_void_p),
+        ("free_range_out", ctypes.c_void_p), ("query_start", ctypes.c_void_p), ("slots", ctypes.c_void_p),
+        ("positions", ctypes.c_void_p), ("status", ctypes.c_void_p),
+    ]
+
+
+class HraAppendParams(ctypes.Structure):
+    """Mirror of hra_append_params (field order and C types as in include/hra.h)."""
+    _fields_ = [
+        ("n_tokens", ctypes.c_int), ("d_c", ctypes.c_int), ("d_rope", ctypes.c_int),
+        ("latent", ctypes.c_void_p), ("krope_in", ctypes.c_void_p),
+        ("latent_stride", ctypes.c_int64), ("krope_in_stride", ctypes.c_int64),
+        ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("rope_theta", ctypes.c_float),
+        ("ckv", ctypes.c_void_p), ("krope", ctypes.c_void_p),
+        ("ckv_stride", ctypes.c_int64), ("krope_stride", ctypes.c_int64), ("cache_rows", ctypes.c_int64),
+        ("cache_dtype", ctypes.c_int), ("ckv_scale", ctypes.c_void_p), ("ckv_scale_stride", ctypes.c_int64),
+        ("scale_block", ctypes.c_int), ("rows_out", ctypes.c_void_p), ("rows_out_stride", ctypes.c_int64),
+    ]
+
+
+class HraLoadParams(ctypes.Structure):
+    """Mirror of hra_load_params (field order and C types as in include/hra.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int), ("max_tokens", ctypes.c_int), ("d_c", ctypes.c_int), ("d_rope", ctypes.c_int),
+        ("ckv", ctypes.c_void_p), ("krope", ctypes.c_void_p),
+        ("ckv_stride", ctypes.c_int64), ("krope_stride", ctypes.c_int64), ("cache_rows", ctypes.c_int64),
+        ("cache_dtype", ctypes.c_int), ("ckv_scale", ctypes.c_void_p), ("ckv_scale_stride", ctypes.c_int64),
+        ("scale_block", ctypes.c_int), ("seq_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("max_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("seq_stride", ctypes.c_int64),
+        ("out", ctypes.c_void_p), ("out_stride", ctypes.c_int64), ("out_seq_stride", ctypes.c_int64),
     ]
 
 
@@ -97,6 +140,10 @@ def load_library() -> ctypes.CDLL:
     lib.hra_prefill_workspace_size.restype = ctypes.c_size_t
     for name in ("mlra_prefill", "hra_check_prefill_status"):
         getattr(lib, name).argtypes = [PP, ctypes.c_void_p]
+        getattr(lib, name).restype = ctypes.c_int
+    for name, cls in (("hra_page_plan", HraPlanParams), ("hra_check_plan_status", HraPlanParams),
+                      ("hra_cache_append", HraAppendParams), ("hra_cache_load", HraLoadParams)):
+        getattr(lib, name).argtypes = [ctypes.POINTER(cls), ctypes.c_void_p]
         getattr(lib, name).restype = ctypes.c_int
     lib.hra_combine_partials.argtypes = [P, ctypes.c_int, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
     lib.hra_combine_partials.restype = ctypes.c_int
@@ -134,18 +181,35 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
+def _cache_format(p, ckv, ckv_scale, scale_block: int) -> None:
+    import torch
+    p.cache_dtype = {torch.int8: HRA_INT8, torch.float8_e4m3fn: HRA_E4M3}.get(ckv.dtype, HRA_BF16)
+    p.scale_block = int(scale_block)
+    if p.cache_dtype == HRA_BF16:
+        return
+    if ckv_scale is None:
+        raise ValueError("an int8 cache needs ckv_scale" if p.cache_dtype == HRA_INT8 else "an e4m3 cache needs ckv_scale")
+    if scale_block > 1:
+        need = (-(-int(ckv.shape[0]) // int(scale_block)), int(ckv.shape[1]) // 128)
+        if (ckv_scale.dtype != torch.float32 or ckv_scale.dim() != 2 or int(ckv_scale.shape[0]) < need[0]
+                or int(ckv_scale.shape[1]) < need[1] or (need[1] > 1 and ckv_scale.stride(1) != 1)):
+            raise ValueError(f"ckv_scale must be float32 {list(need)}, one scale per block of {scale_block} rows and 128 columns")
+    p.ckv_scale, p.ckv_scale_stride = _ptr(ckv_scale), int(ckv_scale.stride(0))
+
+
 def make_params(q, ckv, krope, seq_lens, w_uk, w_uv, out, workspace=None, *, n_branch: int,
                 alpha_q: float = 1.0, alpha_kv: float = 1.0, branch_scale: Optional[float] = None,
                 softmax_scale: float = 0.0, rope_theta: float = 10000.0, block_table=None,
                 page_size: int = 0, seq_stride: int = 0, cache_rows: Optional[int] = None,
                 num_splits: int = 0, wait_limit: int = 0, out_accumulate: bool = False,
                 out_peers=None, ckv_scale=None, q_positions=None, part_o=None,
-                part_lse=None) -> HraDecodeParams:
+                part_lse=None, scale_block: int = 0) -> HraDecodeParams:
     """Fill hra_decode_params from torch tensors (shapes/dtypes as documented in hra.h).
 
     ckv / krope are 2-D row views of the cache (e.g. cache[:, :512], cache[:, 512:]);
     their row strides become ckv_stride / krope_stride.  An int8 ckv selects the quantised
-    cache: ckv_scale is then the fp32 [rows, d_c / 128] view of its block scales.  out_peers: device addresses (ints)
+    cache: ckv_scale is then the fp32 [rows, d_c / 128] view of its block scales; with
+    scale_block (int8 or float8_e4m3fn) it is [rows / scale_block, d_c / 128].  out_peers: device addresses (ints)
     or tensors of other ranks' out buffers for out_accumulate (the array is kept alive on
     the returned object).  q_positions (int32 [B]), part_o (fp32 [B, h, d_c]) and part_lse
     (fp32 [B, h, d_c / 128]) make the call the decode of one token range of longer
@@ -158,11 +222,7 @@ def make_params(q, ckv, krope, seq_lens, w_uk, w_uv, out, workspace=None, *, n_b
     p.d_c, p.d_rope, p.d_nope, p.d_v = int(ckv.shape[1]), int(krope.shape[1]), int(q.shape[2]) - int(krope.shape[1]), int(w_uv.shape[2])
     p.q, p.ckv, p.krope = _ptr(q), _ptr(ckv), _ptr(krope)
     p.ckv_stride, p.krope_stride = int(ckv.stride(0)), int(krope.stride(0))
-    if ckv.dtype == torch.int8:
-        if ckv_scale is None:
-            raise ValueError("an int8 cache needs ckv_scale")
-        p.cache_dtype = HRA_INT8
-        p.ckv_scale, p.ckv_scale_stride = _ptr(ckv_scale), int(ckv_scale.stride(0))
+    _cache_format(p, ckv, ckv_scale, scale_block)
     p.cache_rows = int(ckv.shape[0]) if cache_rows is None else int(cache_rows)
     p.seq_lens = _ptr(seq_lens)
     p.block_table = _ptr(block_table)
@@ -282,3 +342,130 @@ def mlra_prefill(p: HraPrefillParams, stream=None) -> None:
 
 def check_prefill_status(p: HraPrefillParams, stream=None) -> None:
     _check(load_library().hra_check_prefill_status(ctypes.byref(p), ctypes.c_void_p(_stream_handle(stream))))
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _vector(t, n: Optional[int], dtype, name: str) -> None:
+    """t is a contiguous 1-D tensor of dtype with n elements (any number where n is None)."""
+    _need(t.dtype == dtype and t.dim() == 1 and t.is_contiguous() and (n is None or int(t.shape[0]) == n),
+          f"{name} must be a contiguous {dtype} vector" + ("" if n is None else f" of {n}"))
+
+
+def make_plan_params(seq_lens, new_tokens, block_table, free_pages, free_range, seq_lens_out, free_range_out,
+                     query_start, slots, status, *, positions=None, page_size: int) -> HraPlanParams:
+    """Fill hra_plan_params (a step's page plan, see hra.h) from torch tensors: seq_lens,
+    new_tokens and seq_lens_out int32 [B], block_table int32 [B, max_pages] contiguous,
+    free_pages int32 [num_pages], free_range and free_range_out int64 [2], query_start
+    int32 [B + 1], slots (and positions) int32 [max_tokens], status int32 [4].
+    seq_lens_out and free_range_out may be seq_lens and free_range."""
+    import torch
+    B = int(seq_lens.shape[0])
+    for t, n, name in ((seq_lens, B, "seq_lens"), (new_tokens, B, "new_tokens"), (seq_lens_out, B, "seq_lens_out"),
+                       (free_pages, None, "free_pages"), (query_start, B + 1, "query_start"), (slots, None, "slots"),
+                       (status, 4, "status")):
+        _vector(t, n, torch.int32, name)
+    for t, name in ((free_range, "free_range"), (free_range_out, "free_range_out")):
+        _vector(t, 2, torch.int64, name)
+    if positions is not None:
+        _vector(positions, int(slots.shape[0]), torch.int32, "positions")
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.is_contiguous()
+          and int(block_table.shape[0]) == B, f"block_table must be contiguous int32 [{B}, max_pages]")
+    p = HraPlanParams()
+    p.batch, p.page_size, p.max_pages = B, int(page_size), int(block_table.shape[1])
+    p.num_pages, p.max_tokens = int(free_pages.shape[0]), int(slots.shape[0])
+    p.seq_lens, p.new_tokens, p.block_table = _ptr(seq_lens), _ptr(new_tokens), _ptr(block_table)
+    p.free_pages, p.free_range = _ptr(free_pages), _ptr(free_range)
+    p.seq_lens_out, p.free_range_out = _ptr(seq_lens_out), _ptr(free_range_out)
+    p.query_start, p.slots, p.positions, p.status = _ptr(query_start), _ptr(slots), _ptr(positions), _ptr(status)
+    return p
+
+
+def page_plan(p: HraPlanParams, stream=None) -> None:
+    """Plan a step on the device: new block table entries, slots and positions of the new
+    tokens, lengths and page pool after the step.  A refused step is seen in p's status
+    tensor, or with check_plan_status."""
+    _check(load_library().hra_page_plan(ctypes.byref(p), ctypes.c_void_p(_stream_handle(stream))))
+
+
+def check_plan_status(p: HraPlanParams, stream=None) -> None:
+    _check(load_library().hra_check_plan_status(ctypes.byref(p), ctypes.c_void_p(_stream_handle(stream))))
+
+
+def _rows_2d(t, cols: int, dtype, name: str) -> None:
+    _need(t.dim() == 2 and t.dtype == dtype and int(t.shape[1]) == cols and t.stride(1) == 1,
+          f"{name} must be {dtype} [rows, {cols}] with adjacent columns")
+
+
+def _cache_rows(p, ckv, krope, ckv_scale, scale_block: int) -> None:
+    import torch
+    _need(ckv.dtype in (torch.bfloat16, torch.int8, torch.float8_e4m3fn), f"a cache is bfloat16, int8 or float8_e4m3fn, not {ckv.dtype}")
+    _rows_2d(ckv, p.d_c, ckv.dtype, "ckv")
+    _rows_2d(krope, 64, torch.bfloat16, "krope")
+    _need(int(krope.shape[0]) >= int(ckv.shape[0]), "krope has fewer rows than ckv")
+    _cache_format(p, ckv, ckv_scale, scale_block)
+    p.ckv, p.krope = _ptr(ckv), _ptr(krope)
+    p.ckv_stride, p.krope_stride, p.cache_rows = int(ckv.stride(0)), int(krope.stride(0)), int(ckv.shape[0])
+
+
+def make_append_params(latent, krope_in, slots, positions, ckv, krope, *, ckv_scale=None, scale_block: int = 0,
+                       rows_out=None, rope_theta: float = 10000.0) -> HraAppendParams:
+    """Fill hra_append_params (new tokens into the cache, see hra.h) from torch tensors:
+    latent bf16 [n, d_c] and krope_in bf16 [n, 64] (views of one projection output will do),
+    slots and positions int32 [n] (a page plan's), the cache as make_params takes it, and
+    optionally rows_out bf16 [n, d_c + 64] for the rows as the cache stands for them."""
+    import torch
+    p = HraAppendParams()
+    p.n_tokens, p.d_c, p.d_rope = int(latent.shape[0]), int(latent.shape[1]), int(krope_in.shape[1])
+    _rows_2d(latent, p.d_c, torch.bfloat16, "latent")
+    _rows_2d(krope_in, 64, torch.bfloat16, "krope_in")
+    _need(int(krope_in.shape[0]) == p.n_tokens, "latent and krope_in differ in rows")
+    _vector(slots, p.n_tokens, torch.int32, "slots")
+    _vector(positions, p.n_tokens, torch.int32, "positions")
+    _need(int(ckv.shape[1]) == p.d_c, f"ckv has {int(ckv.shape[1])} columns, latent {p.d_c}")
+    _cache_rows(p, ckv, krope, ckv_scale, scale_block)
+    p.latent, p.krope_in = _ptr(latent), _ptr(krope_in)
+    p.latent_stride, p.krope_in_stride = int(latent.stride(0)), int(krope_in.stride(0))
+    p.slots, p.positions, p.rope_theta = _ptr(slots), _ptr(positions), float(rope_theta)
+    if rows_out is not None:
+        _rows_2d(rows_out, p.d_c + 64, torch.bfloat16, "rows_out")
+        _need(int(rows_out.shape[0]) == p.n_tokens, "rows_out and latent differ in rows")
+        p.rows_out, p.rows_out_stride = _ptr(rows_out), int(rows_out.stride(0))
+    return p
+
+
+def cache_append(p: HraAppendParams, stream=None) -> None:
+    """Write new tokens into the cache: latents in the cache's format, RoPE keys turned to
+    their positions."""
+    _check(load_library().hra_cache_append(ctypes.byref(p), ctypes.c_void_p(_stream_handle(stream))))
+
+
+def make_load_params(ckv, krope, seq_lens, out, *, block_table=None, page_size: int = 0, seq_stride: int = 0,
+                     ckv_scale=None, scale_block: int = 0) -> HraLoadParams:
+    """Fill hra_load_params (cached rows back as bf16, see hra.h) from torch tensors: the
+    cache as make_params takes it, seq_lens int32 [B] and out bf16 [B, max_tokens, d_c + 64]."""
+    import torch
+    p = HraLoadParams()
+    p.batch, p.max_tokens, p.d_c, p.d_rope = int(seq_lens.shape[0]), int(out.shape[1]), int(ckv.shape[1]), 64
+    _vector(seq_lens, None, torch.int32, "seq_lens")
+    _need(out.dim() == 3 and out.dtype == torch.bfloat16 and out.stride(2) == 1
+          and (int(out.shape[0]), int(out.shape[2])) == (p.batch, p.d_c + 64),
+          f"out must be bfloat16 [{p.batch}, max_tokens, {p.d_c + 64}] with adjacent columns")
+    _cache_rows(p, ckv, krope, ckv_scale, scale_block)
+    if block_table is not None:
+        _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.is_contiguous()
+              and int(block_table.shape[0]) == p.batch, f"block_table must be contiguous int32 [{p.batch}, max_pages]")
+        p.max_pages = int(block_table.shape[1])
+    p.seq_lens, p.block_table = _ptr(seq_lens), _ptr(block_table)
+    p.page_size, p.seq_stride = int(page_size), int(seq_stride)
+    p.out, p.out_stride, p.out_seq_stride = _ptr(out), int(out.stride(1)), int(out.stride(0))
+    return p
+
+
+def cache_load(p: HraLoadParams, stream=None) -> None:
+    """Read cached rows back as contiguous bf16 rows [C_KV | K_RoPE], the form mlra_prefill
+    takes."""
+    _check(load_library().hra_cache_load(ctypes.byref(p), ctypes.c_void_p(_stream_handle(stream))))

@@ -127,19 +127,30 @@ hra_status validate(const hra_decode_params* p) {
         return fail(HRA_ERR_INVALID_ARG, "out_peers[%d] is NULL or not 16-byte aligned", k);
   }
   if (p->wait_limit < 0) return fail(HRA_ERR_INVALID_ARG, "wait_limit=%d must be >= 0", p->wait_limit);
-  if (p->cache_dtype == HRA_INT8) {
+  if (p->cache_dtype == HRA_INT8 || p->cache_dtype == HRA_E4M3) {
     if (p->d_c / p->n_branch != 128)
-      return fail(HRA_ERR_UNSUPPORTED, "an int8 cache is supported for 128-wide branches (d_c / n_branch = %d)",
+      return fail(HRA_ERR_UNSUPPORTED, "an 8-bit cache is supported for 128-wide branches (d_c / n_branch = %d)",
                   p->d_c / p->n_branch);
     if (p->ckv_scale == nullptr || (reinterpret_cast<uintptr_t>(p->ckv_scale) & 3u) != 0)
       return fail(HRA_ERR_INVALID_ARG, "ckv_scale is NULL or not 4-byte aligned");
     if (p->ckv_scale_stride < p->d_c / 128)
       return fail(HRA_ERR_INVALID_ARG, "ckv_scale_stride=%lld must be >= d_c / 128", (long long)p->ckv_scale_stride);
     if (p->ckv_stride % 16 != 0)
-      return fail(HRA_ERR_INVALID_ARG, "ckv_stride=%lld bytes must be a multiple of 16 for an int8 cache",
+      return fail(HRA_ERR_INVALID_ARG, "ckv_stride=%lld bytes must be a multiple of 16 for an 8-bit cache",
                   (long long)p->ckv_stride);
+    if (p->scale_block < 0 || p->scale_block > 1024 || (p->scale_block > 1 && p->scale_block % 32 != 0))
+      return fail(HRA_ERR_UNSUPPORTED, "scale_block=%d (supported: 0 or 1, or a multiple of 32 up to 1024)", p->scale_block);
+    if (p->scale_block <= 1 && p->cache_dtype == HRA_E4M3)
+      return fail(HRA_ERR_UNSUPPORTED, "an e4m3 cache needs scale_block (one scale per block of rows)");
+    if (p->scale_block > 1) {  // no block may hold rows of two sequences
+      if (p->block_table != nullptr ? p->page_size % p->scale_block != 0
+                                    : p->batch > 1 && p->seq_stride % p->scale_block != 0)
+        return fail(HRA_ERR_INVALID_ARG, "scale_block=%d must divide page_size (contiguous layout: seq_stride)", p->scale_block);
+    }
   } else if (p->cache_dtype != HRA_BF16) {
-    return fail(HRA_ERR_INVALID_ARG, "cache_dtype=%d (HRA_BF16 or HRA_INT8)", (int)p->cache_dtype);
+    return fail(HRA_ERR_INVALID_ARG, "cache_dtype=%d (HRA_BF16, HRA_INT8 or HRA_E4M3)", (int)p->cache_dtype);
+  } else if (p->scale_block > 1 || p->scale_block < 0) {
+    return fail(HRA_ERR_INVALID_ARG, "scale_block=%d needs an 8-bit cache", p->scale_block);
   }
   if (!std::isfinite(p->alpha_q) || !std::isfinite(p->alpha_kv) || !std::isfinite(p->branch_scale) ||
       !std::isfinite(p->softmax_scale) || !(p->rope_theta > 0.f) || !std::isfinite(p->rope_theta))
@@ -234,8 +245,8 @@ hra_status run_decode(const hra_decode_params* p, cudaStream_t stream) {
   if ((st = encode_map(&map_olat, o_lat, dc, 2 * static_cast<int64_t>(h) * B, dc, hra::upproj_seq_chunk())) !=
       HRA_OK)
     return st;
-  const bool int8 = p->cache_dtype == HRA_INT8;
-  // int8: one 128-byte box per 128-wide branch and 32 rows; bf16: 64-column boxes
+  const bool int8 = p->cache_dtype != HRA_BF16;
+  // 8-bit: one 128-byte box per 128-wide branch and 32 rows; bf16: 64-column boxes
   const int box_rows = int8 ? 32 : hra::decode_box_rows(dc / p->n_branch);
   if ((st = encode_map(&map_ckv, p->ckv, dc, p->cache_rows, p->ckv_stride, box_rows, int8, int8 ? 128 : 64)) !=
       HRA_OK)
@@ -291,7 +302,8 @@ hra_status run_decode(const hra_decode_params* p, cudaStream_t stream) {
   da.status = status;
   const uint64_t limit_us = p->wait_limit > 0 ? static_cast<uint64_t>(p->wait_limit) : kDefaultWaitLimitUs;
   da.wait_limit_ns = 1000ull * (limit_us < kMinWaitLimitUs ? kMinWaitLimitUs : limit_us);
-  da.cache_int8 = int8 ? 1 : 0;
+  da.cache_int8 = p->cache_dtype == HRA_E4M3 ? 2 : int8 ? 1 : 0;
+  da.scale_block = p->scale_block > 1 ? p->scale_block : 1;
   da.ckv_scale = int8 ? p->ckv_scale : nullptr;
   da.scale_stride = int8 ? p->ckv_scale_stride : 0;
   if ((e = mark(1)) != cudaSuccess) return cuda_fail(e, "stage event");

@@ -27,9 +27,11 @@ struct DecodeArgs {
   float2* ml_part;            // fp32 [slots, d_c / 128, 128] pairs: (running max in log2 units, row sum)
   int* status;                // device status word
   uint64_t wait_limit_ns;     // global-time budget of one device-side wait
-  int cache_int8;             // 1: the latent cache is int8 with per-(row, 128-column block) scales
-  const float* ckv_scale;     // fp32 scales of row r at ckv_scale + r * scale_stride (int8 cache)
+  int cache_int8;             // 8-bit latent cache: 1 int8, 2 e4m3; 0: bf16
+  const float* ckv_scale;     // 8-bit cache: fp32 scales of row r, one per 128-column block, at
+                              //   ckv_scale + r / scale_block * scale_stride
   long long scale_stride;
+  int scale_block;            // rows that share a scale: 1, or a multiple of 32
 };
 
 // Cache row of the 32-row chunk that starts at token `tok` of sequence s (length L):

@@ -61,10 +61,12 @@ typedef enum {
   HRA_ERR_UNSUPPORTED = -2,     /* shape outside the supported set (see below)           */
   HRA_ERR_WORKSPACE = -3,       /* workspace missing or smaller than hra_workspace_size  */
   HRA_ERR_CUDA = -4,            /* a CUDA runtime/driver call or a launch failed         */
-  HRA_ERR_DEVICE_TIMEOUT = -5   /* a bounded device-side wait expired                    */
+  HRA_ERR_DEVICE_TIMEOUT = -5,  /* a bounded device-side wait expired                    */
+  HRA_ERR_PLAN = -6             /* a page plan was refused on the device                 */
 } hra_status;
 
-typedef enum { HRA_BF16 = 0, HRA_F32 = 1, HRA_INT8 = 2 } hra_dtype;
+/* HRA_E4M3: 8-bit floats of 4 exponent and 3 mantissa bits, no infinities, up to 448. */
+typedef enum { HRA_BF16 = 0, HRA_F32 = 1, HRA_INT8 = 2, HRA_E4M3 = 3 } hra_dtype;
 
 /*
  * Parameters of one decode step.  All pointers are device pointers, 16-byte aligned.
@@ -146,7 +148,9 @@ typedef struct {
      to fp16 (|q * scale| < 65504).  The cache then holds d_c + 2 * d_rope + 4 * d_c / 128
      bytes per token instead of 2 * (d_c + d_rope).                                         */
   hra_dtype cache_dtype;        /* HRA_BF16 (default) or HRA_INT8                          */
-  const float* ckv_scale;       /* fp32 scales, row r's at ckv_scale + r * ckv_scale_stride */
+  const float* ckv_scale;       /* fp32 scales, row r's at ckv_scale + r * ckv_scale_stride
+                                   (with scale_block, at ckv_scale +
+                                   (r / scale_block) * ckv_scale_stride)                  */
   int64_t ckv_scale_stride;     /* floats between consecutive rows' scales, >= d_c / 128   */
 
   /* One sequence split across devices by token range (optional; NULL = off).  A device
@@ -161,6 +165,14 @@ typedef struct {
   const int32_t* q_positions;   /* [B] position of each sequence's query, or NULL: L - 1   */
   float* part_o;                /* fp32 [B, h, d_c], 16-B aligned, or NULL                 */
   float* part_lse;              /* fp32 [B, h, d_c / 128], 16-B aligned, or NULL           */
+
+  /* One scale for each block of scale_block cache rows and 128-column block (0 or 1: one per
+     row, HRA_INT8 only).  scale_block is a multiple of 32 up to 1024 that divides page_size, or in the
+     contiguous layout seq_stride (batch > 1); cache_dtype is HRA_INT8 or HRA_E4M3.  The cache
+     then holds d_c + 2 * d_rope bytes per token.  A scale is finite and >= 0 (a scale that is no
+     number makes the output of the sequences that read it no number); the values it
+     stands for, |code * scale|, stay below 65504.  hra_cache_append writes this format.        */
+  int scale_block;
 } hra_decode_params;
 
 /* Bytes of workspace one call with these parameters needs (0 on invalid parameters).
@@ -251,6 +263,115 @@ HRA_API hra_status mlra_prefill(const hra_prefill_params* p, void* stream /* cud
 /* Synchronize `stream` and read the device status word of p->workspace (as
  * hra_check_device_status does for a decode call). */
 HRA_API hra_status hra_check_prefill_status(const hra_prefill_params* p, void* stream);
+
+/*
+ * Page plan of one step, on the device: from the requests' cached lengths and the tokens that
+ * each brings, the block table's new entries, the cache row (slot) and the position of every
+ * new token, and the page pool after the step.  The pool is a ring of page numbers:
+ * the free pages are free_pages[k % num_pages] for k in [free_range[0], free_range[1]); pages
+ * are taken at its head, in the order of the sequences, and given back at its tail.
+ * new_tokens[b] < 0 ends request b: its pages go back and its length becomes 0 (its table row is
+ * left as it was).
+ * A step that cannot be served is refused as a whole: lengths and pool stay as they were, no
+ * page is taken or given back, every slot is -1, and status says why (hra_check_plan_status
+ * reads it).  Slots and positions behind the last token are -1, so a captured step can be
+ * replayed with any number of tokens up to max_tokens.
+ * seq_lens_out and free_range_out may be seq_lens and free_range themselves; no other buffers may
+ * overlap.  With buffers of their own, the same call can be made again and gives the same plan.
+ * 1 <= batch <= 1024; page_size a multiple of 32; batch * max_pages, max_pages * page_size and
+ * num_pages * page_size below 2^31.  Pointers 4-byte aligned (free_range 8); one launch, no workspace.
+ */
+typedef struct {
+  int batch, page_size, max_pages, num_pages, max_tokens;
+  const int32_t* seq_lens;    /* [B] cached tokens before the step                          */
+  const int32_t* new_tokens;  /* [B] tokens each request brings; < 0 ends the request       */
+  int32_t* block_table;       /* [B, max_pages], updated in place                           */
+  int32_t* free_pages;        /* [num_pages] ring of page numbers, updated in place         */
+  const int64_t* free_range;  /* [2] head and tail of the ring's free pages (ever growing)  */
+  int32_t* seq_lens_out;      /* [B] lengths after the step                                 */
+  int64_t* free_range_out;    /* [2]                                                        */
+  int32_t* query_start;       /* [B + 1] first new token of each request, and their number  */
+  int32_t* slots;             /* [max_tokens] cache row of each new token, or -1            */
+  int32_t* positions;         /* [max_tokens] its position in its sequence, or NULL         */
+  int32_t* status;            /* [4] 0, or: 1 = the cached length of sequence status[1] is
+                                 negative or longer than its table row; 2 = sequence status[1]
+                                 needs more than max_pages pages; 3 = status[2] tokens, over
+                                 max_tokens; 4 = status[2] pages needed, status[3] free; 5 = the
+                                 free range does not describe a ring of num_pages pages     */
+} hra_plan_params;
+
+HRA_API hra_status hra_page_plan(const hra_plan_params* p, void* stream /* cudaStream_t */);
+
+/* Synchronize `stream` and read p->status: HRA_OK, or HRA_ERR_PLAN with the refusal's message. */
+HRA_API hra_status hra_check_plan_status(const hra_plan_params* p, void* stream);
+
+/*
+ * Append: new tokens' latents and RoPE keys into the cache that mlra_decode reads.  Token i
+ * goes to row slots[i] (a slot that is no row of the cache skips the token: padding); its RoPE key is turned
+ * to positions[i], pairs (j, j + 32) by pos * theta^(-2j/64), and stored as bf16.  The latent
+ * is stored as bf16, or in 8 bits: code = the nearest code to x / s, ties to even, with
+ * s = max|x| / 127 (HRA_INT8) or max|x| / 448 (HRA_E4M3) over 128 columns of one token
+ * (scale_block 0 or 1, HRA_INT8) or of one block of scale_block rows.
+ * Blocks grow: a call that writes row 0 of a block starts it anew; one that writes later rows
+ * only keeps the larger of the block's scale and its own tokens', and where that is larger
+ * than the block's was, the rows before the call's first one are brought to it (code' = the
+ * nearest to code * s_old / s).  Rows behind the call's last are left as they were.
+ * The tokens of one block follow one another in the call, and no slot comes twice (their
+ * rows would hold parts of either; a block in two places of the call gets either's scale).
+ * A latent that is no finite number makes its block's scale no finite number.
+ * rows_out (optional): what the cache now stands for, bf16 [n_tokens, d_c + 64] (latent rounded to
+ * bf16, turned RoPE key), the rows that mlra_prefill reads; rows of skipped tokens are left.
+ * d_c in {128, 256, 512}, d_rope = 64; 1 <= n_tokens < 2^31.  latent, krope_in, ckv, krope and
+ * rows_out 16-byte aligned, bf16 strides multiples of 8, 8-bit ones of 16.  One launch, no workspace.
+ */
+typedef struct {
+  int n_tokens, d_c, d_rope;
+  const void* latent;    /* bf16 [n_tokens, d_c], rows latent_stride apart                   */
+  const void* krope_in;  /* bf16 [n_tokens, 64], NOT turned, rows krope_in_stride apart      */
+  int64_t latent_stride, krope_in_stride;  /* elements                                     */
+  const int32_t* slots;      /* [n_tokens]                                                   */
+  const int32_t* positions;  /* [n_tokens]                                                   */
+  float rope_theta;
+  void* ckv;             /* the cache, as in hra_decode_params                               */
+  void* krope;
+  int64_t ckv_stride, krope_stride, cache_rows;
+  hra_dtype cache_dtype;
+  float* ckv_scale;
+  int64_t ckv_scale_stride;
+  int scale_block;
+  void* rows_out;        /* or NULL                                                          */
+  int64_t rows_out_stride;
+} hra_append_params;
+
+HRA_API hra_status hra_cache_append(const hra_append_params* p, void* stream /* cudaStream_t */);
+
+/*
+ * Load: the cached rows of each sequence back as contiguous bf16 rows [C_KV | K_RoPE], the form
+ * mlra_prefill reads: out[b, t] for t < min(seq_lens[b], max_tokens), 8-bit latents as
+ * code * scale rounded once to bf16.  Rows behind a sequence's last are left as they were; a row whose
+ * page is not in the cache is zero.  The cache is described as in hra_decode_params.
+ * d_c in {128, 256, 512}, d_rope = 64; 1 <= batch <= 1024.  out 16-byte aligned, its strides
+ * multiples of 8.  One launch, no workspace.
+ */
+typedef struct {
+  int batch, max_tokens, d_c, d_rope;
+  const void* ckv;
+  const void* krope;
+  int64_t ckv_stride, krope_stride, cache_rows;
+  hra_dtype cache_dtype;
+  const float* ckv_scale;
+  int64_t ckv_scale_stride;
+  int scale_block;
+  const int32_t* seq_lens;
+  const int32_t* block_table;  /* NULL: contiguous                                          */
+  int32_t max_pages, page_size;
+  int64_t seq_stride;
+  void* out;                   /* bf16 [B, max_tokens, d_c + 64]                              */
+  int64_t out_stride;          /* elements between rows, >= d_c + 64                          */
+  int64_t out_seq_stride;      /* elements between sequences                                  */
+} hra_load_params;
+
+HRA_API hra_status hra_cache_load(const hra_load_params* p, void* stream /* cudaStream_t */);
 
 /* Synchronize `stream` and read the device status word of p->workspace.
  * HRA_OK, or HRA_ERR_DEVICE_TIMEOUT if a bounded wait expired during the last call. */
