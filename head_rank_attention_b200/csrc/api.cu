@@ -276,7 +276,7 @@ hra_status run_decode(const hra_decode_params* p, cudaStream_t stream) {
   ab.rope_theta = p->rope_theta;
   ab.d_c = dc;
   ab.tile_prefix = tile_prefix;
-  ab.tile_tokens = hra::decode_tile_tokens(dc / p->n_branch);
+  ab.tile_tokens = hra::decode_tile_tokens(dc / p->n_branch, p->scale_block);
   ab.q_positions = p->q_positions;
   // Programmatic dependent launch lets each kernel start while the previous one drains;
   // the stage-timing mode launches plainly so that its events bracket whole kernels.

@@ -1,0 +1,631 @@
+// decode_block_sm100.cu -- split-KV decode over a latent cache held in 8 bits (int8 or e4m3)
+// with one scale for each block of rows and 128-wide latent head, on tcgen05/TMEM.
+//
+// The step is the decode of decode_split_sm100.cu ("Multi-Head Low-Rank Attention",
+// 方法步骤详情, step 2): a CTA is one 128-wide branch of one group's tiles, the query is
+// fp16, a tile is fp16 in shared memory, and both products are kind::f16 MMAs with fp32
+// accumulation.  What a block scale changes is the arithmetic around them.
+//
+// Scales.  All rows of a 32-row chunk share the scale s = f * 2^e (f in [1, 2)).  The
+// converter writes code * 2^(e - E), which is exact in fp16, with E the largest exponent of the
+// tile's chunks, kept in [kMinExp, kMaxExp]; the RoPE key is divided by sigma = f * 2^E in
+// fp32 and rounded once.  The MMA then gives score / sigma for the latent and the RoPE part
+// alike, and the softmax multiplies by its chunk's sigma: no rounding of a scale enters the
+// scores.  The values need f * 2^E as well: the softmax works on x = score + log2(sigma), so that
+// P = 2^(x - M) times the converted tile is the scaled value, and the denominator adds
+// P / sigma, one multiplication per chunk.  M is then the largest weight times scale, and
+// partial states keep their meaning: (M, l) with O and l both in units of 2^M.
+//
+// Work decomposition: schedule.cuh, with 96-token tiles.  Even and odd tiles of a CTA are two
+// streams, each with its own softmax warpgroup, score buffer, O and (M, l): one stream's
+// softmax runs while the tensor core works for the other, and nothing passes between
+// them until the segment's end, where they are added.  A thread owns one head row of a
+// tile, so that no row is split over threads.
+//
+// TMEM (512 columns): O of the streams [0, 128), [128, 256) | scores [256, 352), [352, 448) |
+// q~ latent fp16 [448, 512).  P (fp16 pairs) is written over the first 48 score columns.
+// The rope query is in shared memory (the 4 rope MMAs read A from there).
+//
+// Warp roles (16 warps, 4 warpgroups):
+//   0-3, 4-7   softmax of stream 0, 1 (thread = head row = TMEM lane)
+//   8-10, 11-13  converters of even and odd tiles (thread = cache row)
+//   14         TMA producer: rows and chunk scales, one batch of 10 tiles ahead
+//   15         TMEM allocator, issuer of both products: QK(i), PV(i - 1), QK(i + 1), ...
+//              in one thread, whose MMAs run in order: QK(i + 1) may overwrite the buffer
+//              that PV(i - 1) reads without a wait.
+// Every wait is bounded, as in decode_split_sm100.cu.
+#include <cstdint>
+
+#include "decode_sm100.h"
+#include "launch.h"
+#include "schedule.cuh"
+#include "sm100.cuh"
+
+namespace hra {
+
+namespace {
+
+constexpr uint32_t kAll = 0xffffffffu;
+
+// E's range.  The rope key is multiplied by 2^-(E + kRopeShift) at most 2^(-kMinExp - kRopeShift)
+// = 2^6 and the rope query by 2^kRopeShift: keys up to 1000 and queries up to 4000 stay in
+// fp16's range whatever the scales.  Below kMinExp codes are shifted down instead (exact until s =
+// 2^-25); above kMaxExp, up.
+constexpr int kMinExp = -10, kMaxExp = 10, kRopeShift = 4;
+
+struct BlockCfg {
+  static constexpr int NT = 96;
+  static constexpr int STAGES = 5;
+  static constexpr int W = 128;
+  static constexpr int BOX_BYTES = NT * 128;            // 64 fp16 columns (or 128 codes) of the tile's rows
+  static constexpr int STAGE_BYTES = 3 * BOX_BYTES;      // latent 0-63, 64-127, rope
+  static constexpr int LOAD_BYTES = 2 * BOX_BYTES;       // codes (in latent box 1's place) and bf16 rope
+  static constexpr int CHUNKS = NT / 32;
+  static constexpr int TMEM_O = 0, TMEM_S = 256, TMEM_Q = 448, TMEM_COLS = 512;
+  static constexpr int WARP_CONV = 8, CONV_WARPS = 3, WARP_PRODUCER = 14, WARP_MMA = 15;
+  static constexpr int THREADS = 512;
+  // setmaxnreg: 256 softmax threads and 256 others share the 128 * 512 registers of the launch
+  static constexpr int SOFTMAX_REGS = 152, OTHER_REGS = 104;
+  static constexpr int QR_BYTES = 128 * 128;
+  static constexpr int BAR_BYTES = 512;
+  static constexpr int ML_BYTES = 2 * 128 * 8;
+  static constexpr int PAR_BYTES = STAGES * CHUNKS * 32;  // ChunkParams
+  static constexpr int MISC_BYTES = BAR_BYTES + ML_BYTES + PAR_BYTES + 4 * (kMaxBatch + 1);
+  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + QR_BYTES + MISC_BYTES;
+  static_assert((SOFTMAX_REGS + OTHER_REGS) * 256 == 128 * THREADS, "register split");
+  static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+};
+
+// What a 32-row chunk of a stage needs besides its bytes; written by the producer.
+struct __align__(32) ChunkParams {
+  float k;          // sigma * softmax scale * log2 e: score / sigma -> log2 units
+  float lambda;     // log2 sigma
+  float inv_sigma;
+  float rope_mul;   // 2^-kRopeShift / sigma
+  uint32_t code_mul;  // 2^(e - E), twice in fp16
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit, volatile int* abort,
+                                          int* status, int where) {
+  const bool ok = mbar_wait(bar, parity, limit, abort, status, where);
+  return __all_sync(kAll, ok);
+}
+
+// The CTA's segments: the tiles [begin, end) of one sequence after another.
+struct Segments {
+  const int* prefix;
+  int B, t_begin, t_end, s;
+  int first, n;  // the current segment's first tile (of all tiles) and number of tiles
+  __device__ Segments(const int* prefix_, int B_, int t_begin_, int t_end_, int s_first)
+      : prefix(prefix_), B(B_), t_begin(t_begin_), t_end(t_end_), s(s_first - 1), first(0), n(0) {}
+  __device__ bool next() {
+    for (++s; s < B && prefix[s] < t_end; ++s) {
+      first = max(t_begin, prefix[s]);
+      n = min(t_end, prefix[s + 1]) - first;
+      if (n > 0) return true;
+    }
+    return false;
+  }
+};
+
+template <int REGS>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
+// Four codes (one word) times a power of two -> four fp16, exactly.
+template <bool E4M3>
+__device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 mul, __half2 bias) {
+  __half2 a, b;
+  if constexpr (E4M3) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+    a = __hmul2(*reinterpret_cast<const __half2*>(&lo), mul);
+    b = __hmul2(*reinterpret_cast<const __half2*>(&hi), mul);
+  } else {
+    // byte v placed as the fp16 1152 + v (see i8x4_to_f16x4); bias = -1152 * mul
+    const uint32_t t = w ^ 0x80808080u;
+    const uint32_t lo = __byte_perm(t, 0x64646464u, 0x4140);
+    const uint32_t hi = __byte_perm(t, 0x64646464u, 0x4342);
+    a = __hfma2(*reinterpret_cast<const __half2*>(&lo), mul, bias);
+    b = __hfma2(*reinterpret_cast<const __half2*>(&hi), mul, bias);
+  }
+  return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
+}
+
+template <bool E4M3>
+__global__ void __launch_bounds__(BlockCfg::THREADS, 1)
+decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_constant__ CUtensorMap map_krope,
+                    const DecodeArgs a) {
+  using C = BlockCfg;
+  constexpr int NT = C::NT, STAGES = C::STAGES, CHUNKS = C::CHUNKS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* q_rope = tiles + STAGES * C::STAGE_BYTES;
+  uint8_t* misc = q_rope + C::QR_BYTES;
+  uint64_t* full = reinterpret_cast<uint64_t*>(misc);
+  uint64_t* empty = full + STAGES;
+  uint64_t* conv = empty + STAGES;   // [STAGES] the stage holds fp16
+  uint64_t* s_full = conv + STAGES;  // [2] per stream
+  uint64_t* p_ready = s_full + 2;    // [2]
+  uint64_t* pv_done = p_ready + 2;   // [2]
+  uint64_t* q_ready = pv_done + 2;   // the segment's query is in place, the last one's O is read
+  uint64_t* ml_bar = q_ready + 1;    // both streams' (M, l) are in shared memory
+  uint64_t* drain = ml_bar + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* never_flag = abort_flag + 1;  // stays 0: exit-path waits ignore the abort flag
+  float2* ml = reinterpret_cast<float2*>(misc + C::BAR_BYTES);  // [2 streams][128]
+  ChunkParams* params = reinterpret_cast<ChunkParams*>(misc + C::BAR_BYTES + C::ML_BYTES);  // [STAGES][CHUNKS]
+  int* prefix = reinterpret_cast<int*>(misc + C::BAR_BYTES + C::ML_BYTES + C::PAR_BYTES);
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int slice = blockIdx.x;  // = branch
+  const int G = gridDim.y;
+  const int g = blockIdx.y;
+  const int B = a.batch;
+  const uint64_t limit = a.wait_limit_ns;
+  int* status = a.status;
+
+  if (warp == 0) tile_prefix_warp(a.seq_lens, B, NT, prefix);
+  if (threadIdx.x == 0) grid_dep_launch();
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < STAGES; ++i) {
+      mbar_init(&full[i], 1);
+      mbar_init(&empty[i], 1);
+      mbar_init(&conv[i], C::CONV_WARPS);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&s_full[b], 1);
+      mbar_init(&p_ready[b], 4);
+      mbar_init(&pv_done[b], 1);
+    }
+    mbar_init(q_ready, 8);
+    mbar_init(ml_bar, 8);
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *never_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == C::WARP_MMA) {
+    tmem_alloc(tmem_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == C::WARP_PRODUCER && lane == 0) {
+    tma_prefetch_desc(&map_ckv);
+    tma_prefetch_desc(&map_krope);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  const int T = prefix[B];
+  const int t_begin = T > 0 ? group_tile_begin(g, G, T) : 0;
+  const int t_end = T > 0 ? group_tile_begin(g + 1, G, T) : 0;
+  const int s_first = (t_begin < t_end) ? seq_of_tile(prefix, B, t_begin) : B;
+
+  if (warp >= C::WARP_CONV) {
+    regs_dec<C::OTHER_REGS>();
+    if (warp == C::WARP_PRODUCER) {
+      // ------------------------------------------------------------------ TMA producer
+      // Each lane finds the cache row and the scale of one 32-row chunk of a batch of 10
+      // tiles, one batch ahead of the tiles lane 0 is issuing.
+      constexpr int TPB = 32 / CHUNKS;
+      const int ntiles = t_end - t_begin;
+      const uint64_t policy = l2_policy_evict_first();
+      const int my_tile = lane / CHUNKS, my_chunk = lane % CHUNKS;
+      auto chunk_row = [&](int it0) {
+        const int t = t_begin + it0 + my_tile;
+        if (my_tile >= TPB || t >= t_end) return static_cast<int>(a.cache_rows);
+        const int s = seq_of_tile(prefix, B, t);
+        return cache_chunk_row(a, s, (t - prefix[s]) * NT + 32 * my_chunk);
+      };
+      // a chunk past its sequence's end has no scale
+      auto chunk_scale = [&](int row) {
+        return row < a.cache_rows ? a.ckv_scale[row / a.scale_block * a.scale_stride + slice] : 0.f;
+      };
+      int rows = chunk_row(0);
+      float scale = chunk_scale(rows);
+      int issued = 0;
+      bool ok = true;
+      for (int it0 = 0; ok && it0 < ntiles; it0 += TPB) {
+        const int rows_next = chunk_row(it0 + TPB);
+        // this lane's chunk: s = f * 2^e; E is the tile's largest e
+        const uint32_t bits = __float_as_uint(scale);
+        const int ex = static_cast<int>(bits >> 23) - 127;  // s >= 0
+        const bool none = bits < 0x00800000u;                 // zero (or subnormal: taken as zero)
+        const bool bad = bits >= 0x7F800000u;                 // Inf, NaN (or negative)
+        const int e = none || bad ? -127 : ex;
+        const float f = bad ? __uint_as_float(0x7FC00000u) : none ? 1.f : __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
+        int E = e;
+#pragma unroll
+        for (int r = 0; r < CHUNKS; ++r) E = max(E, __shfl_sync(kAll, e, min(my_tile * CHUNKS + r, 31)));
+        E = min(max(E, kMinExp), kMaxExp);
+        const float sigma = f * __uint_as_float(static_cast<uint32_t>(E + 127) << 23);
+        ChunkParams cp;
+        cp.k = sigma * a.scale_log2;
+        cp.lambda = log2f(f) + static_cast<float>(E);
+        cp.inv_sigma = 1.f / sigma;
+        cp.rope_mul = cp.inv_sigma * (1.f / (1 << kRopeShift));
+        const __half m = none || bad ? __float2half_rn(0.f)
+                                     : __float2half_rn(__uint_as_float(static_cast<uint32_t>(max(e - E, -30) + 127) << 23));
+        const __half2 m2 = __half2half2(m);
+        cp.code_mul = *reinterpret_cast<const uint32_t*>(&m2);
+        const float scale_next = chunk_scale(rows_next);
+        for (int k = 0; k < TPB && it0 + k < ntiles; ++k) {
+          const int it = it0 + k, stage = it % STAGES;
+          if (it >= STAGES && !warp_wait(&empty[stage], ((it / STAGES) + 1) & 1, limit, abort_flag, status, 1)) {
+            ok = false;
+            break;
+          }
+          int y[CHUNKS];
+#pragma unroll
+          for (int r = 0; r < CHUNKS; ++r) y[r] = __shfl_sync(kAll, rows, k * CHUNKS + r);
+          // written before the stage is armed: the arrive below releases it to the waits on full
+          if (my_tile == k) params[stage * CHUNKS + my_chunk] = cp;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive_expect_tx(&full[stage], C::LOAD_BYTES);
+            uint8_t* dst = tiles + stage * C::STAGE_BYTES;
+#pragma unroll
+            for (int r = 0; r < CHUNKS; ++r) {
+              tma_load_2d(dst + C::BOX_BYTES + r * 4096, &map_ckv, &full[stage], slice * C::W, y[r], policy);
+              tma_load_2d(dst + 2 * C::BOX_BYTES + r * 4096, &map_krope, &full[stage], 0, y[r], policy);
+            }
+          }
+          __syncwarp();
+          issued = it + 1;
+        }
+        rows = rows_next;
+        scale = scale_next;
+      }
+      for (int k = max(0, issued - STAGES); k < issued; ++k) {  // every stage must come back
+        if (ok && !warp_wait(&empty[k % STAGES], (k / STAGES) & 1, limit, abort_flag, status, 2)) ok = false;
+        if (!ok) {  // aborted: wait (bounded, ignoring the abort flag) for the copy itself
+          warp_wait(&full[k % STAGES], (k / STAGES) & 1, kDrainNs, never_flag, status, 3);
+        }
+      }
+    } else if (warp == C::WARP_MMA) {
+      // ------------------------------------------------------------------ MMA issuer
+      if (lane == 0) {
+        constexpr uint32_t idesc_qk = idesc_f16_f32(128, NT, false);
+        constexpr uint32_t idesc_pv = idesc_f16_f32(128, 128, true);
+        const uint32_t tiles_addr = smem_u32(tiles), qr_addr = smem_u32(q_rope);
+        auto issue_pv = [&](int i, bool first) {  // O of tile i's stream (+)= P . latent
+          const int b = i & 1, stage = i % STAGES;
+          if (!mbar_wait(&p_ready[b], (i >> 1) & 1, limit, abort_flag, status, 13)) return false;
+          tc_fence_after();
+          const uint32_t v_base = tiles_addr + stage * C::STAGE_BYTES;
+#pragma unroll
+          for (int k = 0; k < NT / 16; ++k) {
+            const uint64_t bdesc = smem_desc_sw128(v_base + k * 16 * 128, C::BOX_BYTES, 1024);
+            umma_f16_ts(tmem + C::TMEM_O + 128 * b, tmem + C::TMEM_S + NT * b + 8 * k, bdesc, idesc_pv,
+                        (first && k == 0) ? 0u : 1u);
+          }
+          umma_commit(&pv_done[b]);
+          umma_commit(&empty[stage]);  // QK of the tile completed before its P existed
+          return true;
+        };
+        Segments seg(prefix, B, t_begin, t_end, s_first);
+        int i = 0, n_seg = 0;
+        bool ok = true, pending = false, pending_first = false;
+        while (ok && seg.next()) {
+          // the last segment's tiles are through before this one's query is waited for
+          if (pending) ok = issue_pv(i - 1, pending_first);
+          pending = false;
+          if (!ok || !mbar_wait(q_ready, n_seg & 1, limit, abort_flag, status, 10)) {
+            ok = false;
+            break;
+          }
+          for (int k = 0; ok && k < seg.n; ++k, ++i) {
+            const int b = i & 1, stage = i % STAGES;
+            if (!mbar_wait(&conv[stage], (i / STAGES) & 1, limit, abort_flag, status, 11)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t k_base = tiles_addr + stage * C::STAGE_BYTES;
+            const uint32_t d_tmem = tmem + C::TMEM_S + NT * b;
+#pragma unroll
+            for (int ks = 0; ks < C::W / 16; ++ks) {
+              const uint64_t bdesc = smem_desc_sw128(k_base + (ks >> 2) * C::BOX_BYTES + (ks & 3) * 32, 16, 1024);
+              umma_f16_ts(d_tmem, tmem + C::TMEM_Q + ks * 8, bdesc, idesc_qk, ks > 0 ? 1u : 0u);
+            }
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) {
+              const uint64_t adesc = smem_desc_sw128(qr_addr + ks * 32, 16, 1024);
+              const uint64_t bdesc = smem_desc_sw128(k_base + 2 * C::BOX_BYTES + ks * 32, 16, 1024);
+              umma_f16_ss(d_tmem, adesc, bdesc, idesc_qk, 1u);
+            }
+            umma_commit(&s_full[b]);
+            if (pending && !issue_pv(i - 1, pending_first)) ok = false;
+            pending = true;
+            pending_first = k < 2;  // the stream's first tile of the segment
+          }
+          ++n_seg;
+        }
+        if (ok && pending) issue_pv(i - 1, pending_first);
+        umma_commit(drain);
+        mbar_wait(drain, 0, kDrainNs, never_flag, status, 14);
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------ converters
+      // Thread r of a team rewrites row r of the team's tiles in place: 128 codes (latent box
+      // 1) to 128 fp16 (boxes 0 and 1), 64 bf16 rope values to fp16.  The row is read into
+      // registers before it is written.  Latents of rows at or past the sequence end become
+      // zero, so that 0 * NaN cannot reach O; their scores are masked by the softmax.
+      const int team = warp >= C::WARP_CONV + C::CONV_WARPS ? 1 : 0;
+      const int r = threadIdx.x - 32 * (C::WARP_CONV + team * C::CONV_WARPS);
+      const int sw = r & 7;
+      Segments seg(prefix, B, t_begin, t_end, s_first);
+      int i = 0;
+      bool ok = true;
+      while (ok && seg.next()) {
+        const int L = a.seq_lens[seg.s];
+        for (int k = 0; k < seg.n; ++k, ++i) {
+          if ((i & 1) != team) continue;
+          const int stage = i % STAGES;
+          uint8_t* row = tiles + stage * C::STAGE_BYTES + r * 128;
+          const bool valid = r < L - (seg.first + k - prefix[seg.s]) * NT;
+          if (!warp_wait(&full[stage], (i / STAGES) & 1, limit, abort_flag, status, 20)) {
+            ok = false;
+            break;
+          }
+          const ChunkParams& cp = params[stage * CHUNKS + (r >> 5)];
+          const uint32_t mul_bits = cp.code_mul;
+          const __half2 mul = *reinterpret_cast<const __half2*>(&mul_bits);
+          const __half2 bias = __hmul2(mul, __float2half2_rn(-1152.f));
+          const float rope_mul = cp.rope_mul;
+          // codes [64 h, 64 h + 64) fill box h: the first half leaves box 1's codes in place
+#pragma unroll 1
+          for (int h = 0; h < 2; ++h) {
+            uint4 raw[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+              raw[c] = *reinterpret_cast<const uint4*>(row + C::BOX_BYTES + (((4 * h + c) ^ sw) << 4));
+            uint8_t* box = row + h * C::BOX_BYTES;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint2 h0 = codes_to_f16<E4M3>(raw[c].x, mul, bias), h1 = codes_to_f16<E4M3>(raw[c].y, mul, bias);
+              uint2 h2 = codes_to_f16<E4M3>(raw[c].z, mul, bias), h3 = codes_to_f16<E4M3>(raw[c].w, mul, bias);
+              if (!valid) h0 = h1 = h2 = h3 = make_uint2(0u, 0u);
+              *reinterpret_cast<uint4*>(box + (((2 * c) ^ sw) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+              *reinterpret_cast<uint4*>(box + (((2 * c + 1) ^ sw) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
+            }
+          }
+          uint4* rope = reinterpret_cast<uint4*>(row + 2 * C::BOX_BYTES);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4 v = rope[c];
+            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              w[u] = pack_f16x2(__uint_as_float(w[u] << 16) * rope_mul, __uint_as_float(w[u] & 0xFFFF0000u) * rope_mul);
+            rope[c] = v;
+          }
+          fence_proxy_async_smem();
+          warp_arrive(&conv[stage]);
+        }
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax + epilogue
+    regs_inc<C::SOFTMAX_REGS>();
+    // The query comes from the previous kernel, and the partials written here are read by
+    // the previous call's merge: wait for those grids.  The other roles touch no memory
+    // that another kernel of the chain writes.
+    grid_dep_wait();
+    const int b = warp >> 2;          // stream
+    const int row = threadIdx.x & 127;  // head row == TMEM lane
+    const bool live_warp = 32 * (warp & 3) < a.heads;  // some row of the warp is a head
+    const bool live = row < a.heads;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t s_cols = t_row + C::TMEM_S + NT * b, o_cols = t_row + C::TMEM_O + 128 * b;
+    const int q_stride = a.d_c + 64;
+    Segments seg(prefix, B, t_begin, t_end, s_first);
+    int it = 0, n_seg = 0;
+    bool ok = true;
+    while (ok && seg.next()) {
+      const int s = seg.s;
+      const int L = a.seq_lens[s];
+      {  // this row's query: stream 0 stores the latent part, stream 1 the rope part
+        const __half* q = a.q_tilde + (static_cast<long long>(s) * a.heads + min(row, a.heads - 1)) * q_stride;
+        if (b == 0) {
+          const uint4* src = reinterpret_cast<const uint4*>(q + slice * C::W);
+#pragma unroll 1
+          for (int c = 0; c < 2; ++c) {
+            uint32_t w[32];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const uint4 v = live ? __ldg(src + 8 * c + u) : make_uint4(0u, 0u, 0u, 0u);
+              w[4 * u + 0] = v.x; w[4 * u + 1] = v.y; w[4 * u + 2] = v.z; w[4 * u + 3] = v.w;
+            }
+            tmem_st32(t_row + C::TMEM_Q + 32 * c, w);
+          }
+          tmem_st_wait();
+        } else {
+          const uint4* src = reinterpret_cast<const uint4*>(q + a.d_c);
+          const __half2 up = __float2half2_rn(static_cast<float>(1 << kRopeShift));
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4 v = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
+            __half2* h = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) h[u] = __hmul2(h[u], up);
+            *reinterpret_cast<uint4*>(q_rope + row * 128 + ((c ^ (row & 7)) << 4)) = v;
+          }
+          fence_proxy_async_smem();
+        }
+        tc_fence_before();
+        warp_arrive(q_ready);
+      }
+      float M = -INFINITY, l = 0.f;
+      bool first = true;
+      for (int k = 0; k < seg.n; ++k) {
+        const int i = it + k;
+        if ((i & 1) != b) continue;
+        const int stage = i % STAGES;
+        if (!warp_wait(&s_full[b], (i >> 1) & 1, limit, abort_flag, status, 30)) { ok = false; break; }
+        tc_fence_after();
+        if (!live_warp) {  // rows that are no head: their P and O are never read
+          warp_arrive(&p_ready[b]);
+          continue;
+        }
+        // already complete; orders the producer's writes of the chunk parameters before the reads
+        if (!warp_wait(&full[stage], (i / STAGES) & 1, limit, abort_flag, status, 35)) { ok = false; break; }
+        uint32_t sr[NT];
+        tmem_load<NT>(s_cols, sr);
+        float kc[CHUNKS], lam[CHUNKS], inv[CHUNKS];
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+          const float4 p = *reinterpret_cast<const float4*>(&params[stage * CHUNKS + c]);
+          kc[c] = p.x;
+          lam[c] = p.y;
+          inv[c] = p.z;
+        }
+        tmem_ld_wait();
+        const int n_valid = L - (seg.first + k - prefix[s]) * NT;
+        if (n_valid < NT) {
+#pragma unroll
+          for (int u = 0; u < NT; ++u)
+            if (u >= n_valid) sr[u] = __float_as_uint(-INFINITY);
+        }
+        float mt = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+          float m0 = __uint_as_float(sr[32 * c]), m1 = __uint_as_float(sr[32 * c + 1]);
+#pragma unroll
+          for (int u = 2; u + 4 <= 32; u += 4) {
+            m0 = fmax3(m0, __uint_as_float(sr[32 * c + u]), __uint_as_float(sr[32 * c + u + 1]));
+            m1 = fmax3(m1, __uint_as_float(sr[32 * c + u + 2]), __uint_as_float(sr[32 * c + u + 3]));
+          }
+          m0 = fmax3(m0, __uint_as_float(sr[32 * c + 30]), __uint_as_float(sr[32 * c + 31]));
+          mt = fmaxf(mt, fmaf(fmaxf(m0, m1), kc[c], lam[c]));
+        }
+        float factor = 1.f;
+        bool rescale = false;
+        if (first) {
+          M = mt;
+        } else if (mt > M + 8.f) {  // lazy rescale: keep the reference unless it grew by 2^8
+          factor = ex2_approx(M - mt);
+          M = mt;
+          rescale = true;
+        }
+        l *= factor;
+#pragma unroll
+        for (int c = 0; c < CHUNKS; ++c) {
+          const float2 kv = make_float2(kc[c], kc[c]);
+          const float2 off = make_float2(lam[c] - M, lam[c] - M);
+          float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int u = 0; u < 16; ++u) {
+            const float2 x = fma2(make_float2(__uint_as_float(sr[32 * c + 2 * u]), __uint_as_float(sr[32 * c + 2 * u + 1])), kv, off);
+            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+            if (u & 1) s1 = add2(s1, p); else s0 = add2(s0, p);
+            sr[16 * c + u] = pack_f16x2(p.x, p.y);
+          }
+          const float2 st = add2(s0, s1);
+          l = fmaf(inv[c], st.x + st.y, l);
+        }
+        if (__any_sync(kAll, rescale)) {
+          // the stream's earlier P.V must have completed before O is rescaled
+          if (!warp_wait(&pv_done[b], ((i - 2) >> 1) & 1, limit, abort_flag, status, 31)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(o_cols + 16 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int u = 0; u < 16; ++u) o[u] = __float_as_uint(__uint_as_float(o[u]) * factor);
+            tmem_st16(o_cols + 16 * c, o);
+          }
+        }
+        tmem_store<NT / 2>(s_cols, sr);
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&p_ready[b]);
+        first = false;
+      }
+      if (!ok) break;
+      it += seg.n;
+      // segment end: the streams' states are added; stream b writes O columns [64 b, 64 b + 64).
+      // A stream without a tile here may come early: the other one has read the last segment's
+      // states once the query of this one is in place.
+      if (!warp_wait(q_ready, n_seg & 1, limit, abort_flag, status, 36)) { ok = false; break; }
+      ml[b * 128 + row] = make_float2(M, l);
+      warp_arrive(ml_bar);
+      // each stream's last P.V (a stream without a tile in the segment has M = -inf)
+      const int last = it - 1;
+      for (int c = 0; c < 2 && ok; ++c) {
+        const int i = last - c;
+        if (c < seg.n) ok = warp_wait(&pv_done[i & 1], (i >> 1) & 1, limit, abort_flag, status, 32);
+      }
+      if (!ok || !warp_wait(ml_bar, n_seg & 1, limit, abort_flag, status, 34)) { ok = false; break; }
+      tc_fence_after();
+      if (live_warp) {
+        const float2 ml0 = ml[row], ml1 = ml[128 + row];
+        const int b0 = last & 1;                         // a stream that had a tile
+        const bool both = seg.n > 1;
+        const float M_all = both ? fmaxf(ml0.x, ml1.x) : (b0 ? ml1.x : ml0.x);
+        const bool use0 = both || b0 == 0, use1 = both || b0 == 1;
+        const float w0 = use0 ? ex2_approx(ml0.x - M_all) : 0.f, w1 = use1 ? ex2_approx(ml1.x - M_all) : 0.f;
+        const long long slot = static_cast<long long>(g) + s;
+        const long long at = (slot * gridDim.x + slice) * 128 + row;
+        float4* dst = reinterpret_cast<float4*>(a.o_part + at * 128 + 64 * b);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t o0[32], o1[32];
+          tmem_ld32(t_row + C::TMEM_O + 64 * b + 32 * c, o0);
+          tmem_ld32(t_row + C::TMEM_O + 128 + 64 * b + 32 * c, o1);
+          tmem_ld_wait();
+          if (live) {
+            float v[32];
+#pragma unroll
+            for (int u = 0; u < 32; ++u)
+              v[u] = (use0 ? w0 * __uint_as_float(o0[u]) : 0.f) + (use1 ? w1 * __uint_as_float(o1[u]) : 0.f);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) dst[8 * c + u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+          }
+        }
+        if (b == 0 && live)
+          a.ml_part[at] = make_float2(M_all, (use0 ? w0 * ml0.y : 0.f) + (use1 ? w1 * ml1.y : 0.f));
+      }
+      tc_fence_before();
+      ++n_seg;
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::WARP_MMA) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+}  // namespace
+
+int decode_block_tile_tokens() { return BlockCfg::NT; }
+
+cudaError_t launch_decode_block_kernel(const CUtensorMap& map_ckv, const CUtensorMap& map_krope, const DecodeArgs& a,
+                                       int groups, cudaStream_t stream, bool pdl) {
+  using C = BlockCfg;
+  auto kern = a.cache_int8 == 2 ? decode_block_kernel<true> : decode_block_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(kern, dim3(a.d_c / 128, groups), dim3(C::THREADS), C::SMEM_BYTES, stream, pdl, map_ckv,
+                       map_krope, a);
+}
+
+}  // namespace hra

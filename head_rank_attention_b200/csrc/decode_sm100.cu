@@ -495,7 +495,8 @@ cudaError_t launch_decode(const CUtensorMap& map_ckv, const CUtensorMap& map_kro
 
 }  // namespace
 
-int decode_tile_tokens(int branch_width) {
+int decode_tile_tokens(int branch_width, int scale_block) {
+  if (scale_block > 1) return decode_block_tile_tokens();
   return branch_width == 128 ? decode_split_tile_tokens() : (branch_width == 256 ? 80 : 48);
 }
 
@@ -508,7 +509,9 @@ cudaError_t launch_decode_kernel(int n_branch, const CUtensorMap& map_ckv, const
                                  const DecodeArgs& a, int groups, cudaStream_t stream, bool pdl) {
   if (n_branch < 1 || a.d_c % n_branch != 0 || a.d_c % 128 != 0 || a.d_c > 512) return cudaErrorInvalidValue;
   switch (a.d_c / n_branch) {  // branch width
-    case 128: return launch_decode_split_kernel(map_ckv, map_krope, a, groups, stream, pdl);
+    case 128:
+      if (a.scale_block > 1) return launch_decode_block_kernel(map_ckv, map_krope, a, groups, stream, pdl);
+      return launch_decode_split_kernel(map_ckv, map_krope, a, groups, stream, pdl);
     case 256: return launch_decode<2, 80, 4>(map_ckv, map_krope, a, groups, stream, pdl);
     case 512: return launch_decode<1, 48, 4>(map_ckv, map_krope, a, groups, stream, pdl);
     default: return cudaErrorInvalidValue;

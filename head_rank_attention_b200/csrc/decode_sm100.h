@@ -56,8 +56,10 @@ __device__ __forceinline__ int cache_chunk_row(const DecodeArgs& a, int s, int t
   return static_cast<int>(row);
 }
 
-// Tokens per cache tile for a branch width (decides the TMEM and shared-memory budget).
-int decode_tile_tokens(int branch_width);
+// Tokens per cache tile for a branch width (decides the TMEM and shared-memory budget);
+// scale_block as in DecodeArgs.
+int decode_tile_tokens(int branch_width, int scale_block);
+int decode_block_tile_tokens();
 int decode_split_tile_tokens();
 // Rows of one TMA box of the bf16 cache (the tensor maps' box height) for a branch width.
 int decode_box_rows(int branch_width);
@@ -65,6 +67,11 @@ int decode_box_rows(int branch_width);
 // 128-wide-branch kernel (MLRA-4, or a shard of its branches) with an fp16 query and the
 // tile converted to fp16 in shared memory; grid (d_c / 128 branches, groups).
 cudaError_t launch_decode_split_kernel(const CUtensorMap& map_ckv, const CUtensorMap& map_krope,
+                                       const DecodeArgs& a, int groups, cudaStream_t stream, bool pdl);
+
+// 128-wide-branch kernel over an 8-bit cache with one scale per block of rows and 128 columns
+// (a.scale_block > 1); the same grid.
+cudaError_t launch_decode_block_kernel(const CUtensorMap& map_ckv, const CUtensorMap& map_krope,
                                        const DecodeArgs& a, int groups, cudaStream_t stream, bool pdl);
 
 // Launch the decode kernel on grid (d_c / 128 slices, `groups` KV splits); pdl:

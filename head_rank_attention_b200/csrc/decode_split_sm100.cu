@@ -124,17 +124,13 @@ __device__ __forceinline__ void drain_mmas(uint64_t* bar, volatile int* never, i
   mbar_wait(bar, 0, kDrainNs, never, status, where);
 }
 
-// FMT: bf16 cache, int8 with one scale per row and 128-column block, or int8 / e4m3 with one
-// scale per block of a.scale_block rows (a multiple of the 32 rows of a TMA chunk).
-enum SplitFormat : int { kBf16 = 0, kInt8Row = 1, kInt8Block = 2, kE4m3Block = 3 };
-
-template <SplitFormat FMT>
+// INT8: the latent cache is int8 with per-(row, 128-column block) scales (a.cache_int8 = 1).
+template <bool INT8>
 __global__ void __launch_bounds__(SplitCfg::THREADS, 1)
 decode_split_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_constant__ CUtensorMap map_krope,
                     const DecodeArgs a) {
   using C = SplitCfg;
   constexpr int NT = C::NT, STAGES = C::STAGES, HALF = NT / 2;
-  constexpr bool INT8 = FMT != kBf16;  // 8-bit latents
   extern __shared__ uint8_t smem_raw[];
   uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* misc = tiles + STAGES * C::STAGE_BYTES;
@@ -222,16 +218,10 @@ decode_split_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
     // int8 cache: the 32 block scales of this lane's chunk (0 for rows past the cache),
     // loaded one batch ahead like the rows themselves
     auto chunk_scales = [&](int crow, float* sc) {
-      if constexpr (FMT >= kInt8Block) {
-        const float s = crow < a.cache_rows ? a.ckv_scale[crow / a.scale_block * a.scale_stride + slice] : 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) sc[i] = s;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          sc[i] = crow + i < a.cache_rows ? a.ckv_scale[(static_cast<long long>(crow) + i) * a.scale_stride + slice]
-                                          : 0.f;
-      }
+      for (int i = 0; i < 32; ++i)
+        sc[i] = crow + i < a.cache_rows ? a.ckv_scale[(static_cast<long long>(crow) + i) * a.scale_stride + slice]
+                                        : 0.f;
     };
     int rows = chunk_row(0);
     float sc[INT8 ? 32 : 1];
@@ -395,7 +385,7 @@ decode_split_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
             uint32_t h[8];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const uint2 f = FMT == kE4m3Block ? e4m3x4_to_f16x4(wv[q], s2) : i8x4_to_f16x4(wv[q], s2);
+              const uint2 f = i8x4_to_f16x4(wv[q], s2);
               h[2 * q] = f.x;
               h[2 * q + 1] = f.y;
             }
@@ -604,10 +594,7 @@ int decode_split_tile_tokens() { return SplitCfg::NT; }
 cudaError_t launch_decode_split_kernel(const CUtensorMap& map_ckv, const CUtensorMap& map_krope,
                                        const DecodeArgs& a, int groups, cudaStream_t stream, bool pdl) {
   using C = SplitCfg;
-  auto kern = a.cache_int8 == 0   ? decode_split_kernel<kBf16>
-              : a.cache_int8 == 2 ? decode_split_kernel<kE4m3Block>
-              : a.scale_block > 1 ? decode_split_kernel<kInt8Block>
-                                  : decode_split_kernel<kInt8Row>;
+  auto kern = a.cache_int8 ? decode_split_kernel<true> : decode_split_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(a.d_c / 128, groups), dim3(C::THREADS), C::SMEM_BYTES, stream, pdl, map_ckv,

@@ -366,15 +366,6 @@ __device__ __forceinline__ uint2 i8x4_to_f16x4(uint32_t w, __half2 scale) {
   __half2 b = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&hi), bias), scale);
   return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
 }
-// Four e4m3 values times a scale -> four fp16 (exact, then one fp16 rounding).
-__device__ __forceinline__ uint2 e4m3x4_to_f16x4(uint32_t w, __half2 scale) {
-  uint32_t lo, hi;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(lo) : "h"(static_cast<uint16_t>(w & 0xFFFFu)));
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(hi) : "h"(static_cast<uint16_t>(w >> 16)));
-  __half2 a = __hmul2(*reinterpret_cast<const __half2*>(&lo), scale);
-  __half2 b = __hmul2(*reinterpret_cast<const __half2*>(&hi), scale);
-  return make_uint2(*reinterpret_cast<uint32_t*>(&a), *reinterpret_cast<uint32_t*>(&b));
-}
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
