@@ -30,9 +30,9 @@
 //   0-3, 4-7   softmax of stream 0, 1 (thread = head row = TMEM lane)
 //   8-10, 11-13  converters of even and odd tiles (thread = cache row)
 //   14         TMA producer: rows and chunk scales, one batch of 10 tiles ahead
-//   15         TMEM allocator, issuer of both products: QK(i), PV(i - 1), QK(i + 1), ...
-//              in one thread, whose MMAs run in order: QK(i + 1) may overwrite the buffer
-//              that PV(i - 1) reads without a wait.
+//   15         TMEM allocator, issuer of both products: PV(i), QK(i + 2), PV(i + 1), ...
+//              in one thread, whose MMAs run in order: QK(i + 2) may overwrite the buffer
+//              that PV(i) reads without a wait.
 // Every wait is bounded, as in decode_split_sm100.cu.
 #include <cstdint>
 
@@ -55,11 +55,14 @@ constexpr int kMinExp = -10, kMaxExp = 10, kRopeShift = 4;
 
 struct BlockCfg {
   static constexpr int NT = 96;
-  static constexpr int STAGES = 5;
   static constexpr int W = 128;
-  static constexpr int BOX_BYTES = NT * 128;            // 64 fp16 columns (or 128 codes) of the tile's rows
-  static constexpr int STAGE_BYTES = 3 * BOX_BYTES;      // latent 0-63, 64-127, rope
-  static constexpr int LOAD_BYTES = 2 * BOX_BYTES;       // codes (in latent box 1's place) and bf16 rope
+  static constexpr int BOX_BYTES = NT * 128;            // 64 16-bit columns (or 128 codes) of the tile's rows
+  // Two rings.  A tile's copy (codes, and the RoPE key, converted in place) is held until its
+  // QK has run; its fp16 latent (columns 0-63, 64-127) from the conversion until its P.V has.
+  // One ring for both (36 KB a tile, held 7900 cycles from copy to P.V) made 1980 cycles a tile.
+    static constexpr int RAW = 4, LAT = 4;
+  static constexpr int RAW_BYTES = 2 * BOX_BYTES, LAT_BYTES = 2 * BOX_BYTES;
+  static constexpr int PAR = 8;  // chunk parameters outlive the copy: until the tile's softmax
   static constexpr int CHUNKS = NT / 32;
   static constexpr int TMEM_O = 0, TMEM_S = 256, TMEM_Q = 448, TMEM_COLS = 512;
   static constexpr int WARP_CONV = 8, CONV_WARPS = 3, WARP_PRODUCER = 14, WARP_MMA = 15;
@@ -69,11 +72,16 @@ struct BlockCfg {
   static constexpr int QR_BYTES = 128 * 128;
   static constexpr int BAR_BYTES = 512;
   static constexpr int ML_BYTES = 2 * 128 * 8;
-  static constexpr int PAR_BYTES = STAGES * CHUNKS * 32;  // ChunkParams
+  static constexpr int PAR_BYTES = PAR * CHUNKS * 32;  // ChunkParams
   static constexpr int MISC_BYTES = BAR_BYTES + ML_BYTES + PAR_BYTES + 4 * (kMaxBatch + 1);
-  static constexpr int SMEM_BYTES = 1024 + STAGES * STAGE_BYTES + QR_BYTES + MISC_BYTES;
+  static constexpr int SMEM_BYTES = 1024 + RAW * RAW_BYTES + LAT * LAT_BYTES + QR_BYTES + MISC_BYTES;
   static_assert((SOFTMAX_REGS + OTHER_REGS) * 256 == 128 * THREADS, "register split");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
+  static_assert(PAR >= RAW + 4, "chunk parameters");
+  // A team waits only for its own tiles' copies, and copies may land out of order: were a stage
+  // of that ring shared by the teams, one could take the other's pending phase of it for its
+  // own.  (P.V's complete in order, so the other ring needs no such care.)
+  static_assert(RAW % 2 == 0, "a stage belongs to one converter team");
 };
 
 // What a 32-row chunk of a stage needs besides its bytes; written by the producer.
@@ -117,6 +125,37 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
+// D[tmem] (+)= A * B with A in tensor or shared memory, without the output lane mask that the
+// forms in sm100.cuh pass.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// One lane of the warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}\n" : "=r"(p));
+  return p != 0;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  uint64_t r;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;"
+      : "=l"(r)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&r);
+}
+
 // Four codes (one word) times a power of two -> four fp16, exactly.
 template <bool E4M3>
 __device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 mul, __half2 bias) {
@@ -145,18 +184,18 @@ __global__ void __launch_bounds__(BlockCfg::THREADS, 1)
 decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_constant__ CUtensorMap map_krope,
                     const DecodeArgs a) {
   using C = BlockCfg;
-  constexpr int NT = C::NT, STAGES = C::STAGES, CHUNKS = C::CHUNKS;
+  constexpr int NT = C::NT, RAW = C::RAW, LAT = C::LAT, CHUNKS = C::CHUNKS;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* tiles = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t* q_rope = tiles + STAGES * C::STAGE_BYTES;
+  uint8_t* raws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* lats = raws + RAW * C::RAW_BYTES;
+  uint8_t* q_rope = lats + LAT * C::LAT_BYTES;
   uint8_t* misc = q_rope + C::QR_BYTES;
   uint64_t* full = reinterpret_cast<uint64_t*>(misc);
-  uint64_t* empty = full + STAGES;
-  uint64_t* conv = empty + STAGES;   // [STAGES] the stage holds fp16
-  uint64_t* s_full = conv + STAGES;  // [2] per stream
-  uint64_t* p_ready = s_full + 2;    // [2]
-  uint64_t* pv_done = p_ready + 2;   // [2]
-  uint64_t* q_ready = pv_done + 2;   // the segment's query is in place, the last one's O is read
+  uint64_t* qk_done = full + RAW;    // [RAW] the tile's scores are there, its copy has been read
+  uint64_t* conv = qk_done + RAW;    // [LAT] the latent (and the copy's rope part) is fp16
+  uint64_t* pv_done = conv + LAT;    // [LAT] O has the tile, its latent has been read
+  uint64_t* p_ready = pv_done + LAT; // [2] per stream
+  uint64_t* q_ready = p_ready + 2;   // the segment's query is in place, the last one's O is read
   uint64_t* ml_bar = q_ready + 1;    // both streams' (M, l) are in shared memory
   uint64_t* drain = ml_bar + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
@@ -178,16 +217,15 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
   if (warp == 0) tile_prefix_warp(a.seq_lens, B, NT, prefix);
   if (threadIdx.x == 0) grid_dep_launch();
   if (threadIdx.x == 32) {
-    for (int i = 0; i < STAGES; ++i) {
+    for (int i = 0; i < RAW; ++i) {
       mbar_init(&full[i], 1);
-      mbar_init(&empty[i], 1);
+      mbar_init(&qk_done[i], 1);
+    }
+    for (int i = 0; i < LAT; ++i) {
       mbar_init(&conv[i], C::CONV_WARPS);
+      mbar_init(&pv_done[i], 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(&s_full[b], 1);
-      mbar_init(&p_ready[b], 4);
-      mbar_init(&pv_done[b], 1);
-    }
+    for (int b = 0; b < 2; ++b) mbar_init(&p_ready[b], 4);
     mbar_init(q_ready, 8);
     mbar_init(ml_bar, 8);
     mbar_init(drain, 1);
@@ -262,8 +300,8 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
         cp.code_mul = *reinterpret_cast<const uint32_t*>(&m2);
         const float scale_next = chunk_scale(rows_next);
         for (int k = 0; k < TPB && it0 + k < ntiles; ++k) {
-          const int it = it0 + k, stage = it % STAGES;
-          if (it >= STAGES && !warp_wait(&empty[stage], ((it / STAGES) + 1) & 1, limit, abort_flag, status, 1)) {
+          const int it = it0 + k, stage = it % RAW;
+          if (it >= RAW && !warp_wait(&qk_done[stage], ((it / RAW) + 1) & 1, limit, abort_flag, status, 1)) {
             ok = false;
             break;
           }
@@ -271,15 +309,15 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
 #pragma unroll
           for (int r = 0; r < CHUNKS; ++r) y[r] = __shfl_sync(kAll, rows, k * CHUNKS + r);
           // written before the stage is armed: the arrive below releases it to the waits on full
-          if (my_tile == k) params[stage * CHUNKS + my_chunk] = cp;
+          if (my_tile == k) params[it % C::PAR * CHUNKS + my_chunk] = cp;
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive_expect_tx(&full[stage], C::LOAD_BYTES);
-            uint8_t* dst = tiles + stage * C::STAGE_BYTES;
+            mbar_arrive_expect_tx(&full[stage], C::RAW_BYTES);
+            uint8_t* dst = raws + stage * C::RAW_BYTES;
 #pragma unroll
             for (int r = 0; r < CHUNKS; ++r) {
-              tma_load_2d(dst + C::BOX_BYTES + r * 4096, &map_ckv, &full[stage], slice * C::W, y[r], policy);
-              tma_load_2d(dst + 2 * C::BOX_BYTES + r * 4096, &map_krope, &full[stage], 0, y[r], policy);
+              tma_load_2d(dst + r * 4096, &map_ckv, &full[stage], slice * C::W, y[r], policy);
+              tma_load_2d(dst + C::BOX_BYTES + r * 4096, &map_krope, &full[stage], 0, y[r], policy);
             }
           }
           __syncwarp();
@@ -288,81 +326,79 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
         rows = rows_next;
         scale = scale_next;
       }
-      for (int k = max(0, issued - STAGES); k < issued; ++k) {  // every stage must come back
-        if (ok && !warp_wait(&empty[k % STAGES], (k / STAGES) & 1, limit, abort_flag, status, 2)) ok = false;
+      for (int k = max(0, issued - RAW); k < issued; ++k) {  // every stage must come back
+        if (ok && !warp_wait(&qk_done[k % RAW], (k / RAW) & 1, limit, abort_flag, status, 2)) ok = false;
         if (!ok) {  // aborted: wait (bounded, ignoring the abort flag) for the copy itself
-          warp_wait(&full[k % STAGES], (k / STAGES) & 1, kDrainNs, never_flag, status, 3);
+          warp_wait(&full[k % RAW], (k / RAW) & 1, kDrainNs, never_flag, status, 3);
         }
       }
     } else if (warp == C::WARP_MMA) {
       // ------------------------------------------------------------------ MMA issuer
-      if (lane == 0) {
-        constexpr uint32_t idesc_qk = idesc_f16_f32(128, NT, false);
-        constexpr uint32_t idesc_pv = idesc_f16_f32(128, 128, true);
-        const uint32_t tiles_addr = smem_u32(tiles), qr_addr = smem_u32(q_rope);
-        auto issue_pv = [&](int i, bool first) {  // O of tile i's stream (+)= P . latent
-          const int b = i & 1, stage = i % STAGES;
-          if (!mbar_wait(&p_ready[b], (i >> 1) & 1, limit, abort_flag, status, 13)) return false;
-          tc_fence_after();
-          const uint32_t v_base = tiles_addr + stage * C::STAGE_BYTES;
-#pragma unroll
-          for (int k = 0; k < NT / 16; ++k) {
-            const uint64_t bdesc = smem_desc_sw128(v_base + k * 16 * 128, C::BOX_BYTES, 1024);
-            umma_f16_ts(tmem + C::TMEM_O + 128 * b, tmem + C::TMEM_S + NT * b + 8 * k, bdesc, idesc_pv,
-                        (first && k == 0) ? 0u : 1u);
-          }
-          umma_commit(&pv_done[b]);
-          umma_commit(&empty[stage]);  // QK of the tile completed before its P existed
-          return true;
-        };
-        Segments seg(prefix, B, t_begin, t_end, s_first);
-        int i = 0, n_seg = 0;
-        bool ok = true, pending = false, pending_first = false;
-        while (ok && seg.next()) {
-          // the last segment's tiles are through before this one's query is waited for
-          if (pending) ok = issue_pv(i - 1, pending_first);
-          pending = false;
-          if (!ok || !mbar_wait(q_ready, n_seg & 1, limit, abort_flag, status, 10)) {
+      // The whole warp walks the tiles, so that what an MMA needs is uniform; one lane issues.
+      constexpr uint32_t idesc_qk = idesc_f16_f32(128, NT, false);
+      constexpr uint32_t idesc_pv = idesc_f16_f32(128, 128, true);
+      const uint32_t t0 = __shfl_sync(kAll, tmem, 0);
+      const uint64_t k_desc0 = smem_desc_sw128(smem_u32(lats), 16, 1024);
+      const uint64_t v_desc0 = smem_desc_sw128(smem_u32(lats), C::BOX_BYTES, 1024);
+      const uint64_t kr_desc0 = smem_desc_sw128(smem_u32(raws) + C::BOX_BYTES, 16, 1024);
+      const uint64_t qr_desc = smem_desc_sw128(smem_u32(q_rope), 16, 1024);
+      // descriptors count 16 bytes
+      constexpr uint32_t LAT_STEP = C::LAT_BYTES >> 4, RAW_STEP = C::RAW_BYTES >> 4, BOX_STEP = C::BOX_BYTES >> 4;
+      Segments seg(prefix, B, t_begin, t_end, s_first);
+      int i = 0, n_seg = 0;  // i: the segment's first tile
+      bool ok = true;
+      while (ok && seg.next()) {
+        if (!warp_wait(q_ready, n_seg & 1, limit, abort_flag, status, 10)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int n = __shfl_sync(kAll, seg.n, 0);
+        // P.V of a tile and QK of the one two on (the same buffer) are issued together, and their
+        // commits after both: nothing stands between P and the stream's next scores.
+        for (int k = 0; k < n + 2; ++k) {
+          const int j = i + k, v = j - 2;
+          const bool qk = k < n, pv = k >= 2 && k - 2 < n;
+          if ((qk && !warp_wait(&conv[j % LAT], (j / LAT) & 1, limit, abort_flag, status, 11)) ||
+              (pv && !warp_wait(&p_ready[v & 1], (v >> 1) & 1, limit, abort_flag, status, 13))) {
             ok = false;
             break;
           }
-          for (int k = 0; ok && k < seg.n; ++k, ++i) {
-            const int b = i & 1, stage = i % STAGES;
-            if (!mbar_wait(&conv[stage], (i / STAGES) & 1, limit, abort_flag, status, 11)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            const uint32_t k_base = tiles_addr + stage * C::STAGE_BYTES;
-            const uint32_t d_tmem = tmem + C::TMEM_S + NT * b;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t s_tmem = t0 + C::TMEM_S + NT * (j & 1);
+            if (pv) {  // O of the stream (+)= P . latent
+              const uint64_t v_desc = v_desc0 + v % LAT * LAT_STEP;
+              const uint32_t o = t0 + C::TMEM_O + 128 * (j & 1);
 #pragma unroll
-            for (int ks = 0; ks < C::W / 16; ++ks) {
-              const uint64_t bdesc = smem_desc_sw128(k_base + (ks >> 2) * C::BOX_BYTES + (ks & 3) * 32, 16, 1024);
-              umma_f16_ts(d_tmem, tmem + C::TMEM_Q + ks * 8, bdesc, idesc_qk, ks > 0 ? 1u : 0u);
+              for (int x = 0; x < NT / 16; ++x)  // 16 rows of 128 bytes on
+                mma_ts(o, s_tmem + 8 * x, v_desc + x * (16 * 128 >> 4), idesc_pv, (k < 4 && x == 0) ? 0u : 1u);
             }
+            if (qk) {
+              const uint64_t k_desc = k_desc0 + j % LAT * LAT_STEP, kr_desc = kr_desc0 + j % RAW * RAW_STEP;
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks) {
-              const uint64_t adesc = smem_desc_sw128(qr_addr + ks * 32, 16, 1024);
-              const uint64_t bdesc = smem_desc_sw128(k_base + 2 * C::BOX_BYTES + ks * 32, 16, 1024);
-              umma_f16_ss(d_tmem, adesc, bdesc, idesc_qk, 1u);
+              for (int x = 0; x < C::W / 16; ++x)
+                mma_ts(s_tmem, t0 + C::TMEM_Q + x * 8, k_desc + (x >> 2) * BOX_STEP + (x & 3) * 2, idesc_qk, x > 0 ? 1u : 0u);
+#pragma unroll
+              for (int x = 0; x < 4; ++x) mma_ss(s_tmem, qr_desc + x * 2, kr_desc + x * 2, idesc_qk, 1u);
+              umma_commit(&qk_done[j % RAW]);
             }
-            umma_commit(&s_full[b]);
-            if (pending && !issue_pv(i - 1, pending_first)) ok = false;
-            pending = true;
-            pending_first = k < 2;  // the stream's first tile of the segment
+            if (pv) umma_commit(&pv_done[v % LAT]);
           }
-          ++n_seg;
+          __syncwarp();
         }
-        if (ok && pending) issue_pv(i - 1, pending_first);
+        i += n;
+        ++n_seg;
+      }
+      if (elect_one()) {
         umma_commit(drain);
         mbar_wait(drain, 0, kDrainNs, never_flag, status, 14);
       }
       __syncwarp();
     } else {
       // ------------------------------------------------------------------ converters
-      // Thread r of a team rewrites row r of the team's tiles in place: 128 codes (latent box
-      // 1) to 128 fp16 (boxes 0 and 1), 64 bf16 rope values to fp16.  The row is read into
-      // registers before it is written.  Latents of rows at or past the sequence end become
+      // Thread r of a team converts row r of the team's tiles: 128 codes to fp16, 64 bf16 rope
+      // values to fp16 in place.  Latents of rows at or past the sequence end become
       // zero, so that 0 * NaN cannot reach O; their scores are masked by the softmax.
       const int team = warp >= C::WARP_CONV + C::CONV_WARPS ? 1 : 0;
       const int r = threadIdx.x - 32 * (C::WARP_CONV + team * C::CONV_WARPS);
@@ -374,44 +410,44 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
         const int L = a.seq_lens[seg.s];
         for (int k = 0; k < seg.n; ++k, ++i) {
           if ((i & 1) != team) continue;
-          const int stage = i % STAGES;
-          uint8_t* row = tiles + stage * C::STAGE_BYTES + r * 128;
+          const int stage = i % LAT;
+          uint8_t* row = raws + i % RAW * C::RAW_BYTES + r * 128;
+          uint8_t* lat = lats + stage * C::LAT_BYTES + r * 128;
           const bool valid = r < L - (seg.first + k - prefix[seg.s]) * NT;
-          if (!warp_wait(&full[stage], (i / STAGES) & 1, limit, abort_flag, status, 20)) {
+          if ((i >= LAT && !warp_wait(&pv_done[stage], ((i / LAT) + 1) & 1, limit, abort_flag, status, 21)) ||
+              !warp_wait(&full[i % RAW], (i / RAW) & 1, limit, abort_flag, status, 20)) {
             ok = false;
             break;
           }
-          const ChunkParams& cp = params[stage * CHUNKS + (r >> 5)];
+          const ChunkParams& cp = params[i % C::PAR * CHUNKS + (r >> 5)];
           const uint32_t mul_bits = cp.code_mul;
           const __half2 mul = *reinterpret_cast<const __half2*>(&mul_bits);
           const __half2 bias = __hmul2(mul, __float2half2_rn(-1152.f));
           const float rope_mul = cp.rope_mul;
-          // codes [64 h, 64 h + 64) fill box h: the first half leaves box 1's codes in place
-#pragma unroll 1
-          for (int h = 0; h < 2; ++h) {
-            uint4 raw[4];
+          uint4 raw[8];
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              raw[c] = *reinterpret_cast<const uint4*>(row + C::BOX_BYTES + (((4 * h + c) ^ sw) << 4));
-            uint8_t* box = row + h * C::BOX_BYTES;
+          for (int c = 0; c < 8; ++c) raw[c] = *reinterpret_cast<const uint4*>(row + ((c ^ sw) << 4));
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint2 h0 = codes_to_f16<E4M3>(raw[c].x, mul, bias), h1 = codes_to_f16<E4M3>(raw[c].y, mul, bias);
-              uint2 h2 = codes_to_f16<E4M3>(raw[c].z, mul, bias), h3 = codes_to_f16<E4M3>(raw[c].w, mul, bias);
-              if (!valid) h0 = h1 = h2 = h3 = make_uint2(0u, 0u);
-              *reinterpret_cast<uint4*>(box + (((2 * c) ^ sw) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
-              *reinterpret_cast<uint4*>(box + (((2 * c + 1) ^ sw) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
-            }
+          for (int c = 0; c < 8; ++c) {  // codes [16 c, 16 c + 16) -> fp16 chunks 2 c, 2 c + 1 of 16
+            uint2 h0 = codes_to_f16<E4M3>(raw[c].x, mul, bias), h1 = codes_to_f16<E4M3>(raw[c].y, mul, bias);
+            uint2 h2 = codes_to_f16<E4M3>(raw[c].z, mul, bias), h3 = codes_to_f16<E4M3>(raw[c].w, mul, bias);
+            if (!valid) h0 = h1 = h2 = h3 = make_uint2(0u, 0u);
+            uint8_t* box = lat + (c >> 2) * C::BOX_BYTES;
+            *reinterpret_cast<uint4*>(box + ((((2 * c) & 7) ^ sw) << 4)) = make_uint4(h0.x, h0.y, h1.x, h1.y);
+            *reinterpret_cast<uint4*>(box + ((((2 * c + 1) & 7) ^ sw) << 4)) = make_uint4(h2.x, h2.y, h3.x, h3.y);
           }
-          uint4* rope = reinterpret_cast<uint4*>(row + 2 * C::BOX_BYTES);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) raw[c] = *reinterpret_cast<const uint4*>(row + C::BOX_BYTES + ((c ^ sw) << 4));
+          const float2 rm = make_float2(rope_mul, rope_mul);
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
-            uint4 v = rope[c];
-            uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+            uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
-              w[u] = pack_f16x2(__uint_as_float(w[u] << 16) * rope_mul, __uint_as_float(w[u] & 0xFFFF0000u) * rope_mul);
-            rope[c] = v;
+            for (int u = 0; u < 4; ++u) {
+              const float2 x = mul2(make_float2(__uint_as_float(w[u] << 16), __uint_as_float(w[u] & 0xFFFF0000u)), rm);
+              w[u] = pack_f16x2(x.x, x.y);
+            }
+            *reinterpret_cast<uint4*>(row + C::BOX_BYTES + ((c ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
           fence_proxy_async_smem();
           warp_arrive(&conv[stage]);
@@ -474,21 +510,22 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
       for (int k = 0; k < seg.n; ++k) {
         const int i = it + k;
         if ((i & 1) != b) continue;
-        const int stage = i % STAGES;
-        if (!warp_wait(&s_full[b], (i >> 1) & 1, limit, abort_flag, status, 30)) { ok = false; break; }
+        if (!warp_wait(&qk_done[i % RAW], (i / RAW) & 1, limit, abort_flag, status, 30)) { ok = false; break; }
         tc_fence_after();
         if (!live_warp) {  // rows that are no head: their P and O are never read
           warp_arrive(&p_ready[b]);
           continue;
         }
-        // already complete; orders the producer's writes of the chunk parameters before the reads
-        if (!warp_wait(&full[stage], (i / STAGES) & 1, limit, abort_flag, status, 35)) { ok = false; break; }
+        // already complete; orders the producer's writes of the chunk parameters (which the
+        // converters have seen) before the reads.  The place of tile i + PAR is written after QK(i + RAW),
+        // which comes after this stream's softmax of tile i + 2.
+        if (!warp_wait(&conv[i % LAT], (i / LAT) & 1, limit, abort_flag, status, 35)) { ok = false; break; }
         uint32_t sr[NT];
         tmem_load<NT>(s_cols, sr);
         float kc[CHUNKS], lam[CHUNKS], inv[CHUNKS];
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
-          const float4 p = *reinterpret_cast<const float4*>(&params[stage * CHUNKS + c]);
+          const float4 p = *reinterpret_cast<const float4*>(&params[i % C::PAR * CHUNKS + c]);
           kc[c] = p.x;
           lam[c] = p.y;
           inv[c] = p.z;
@@ -539,7 +576,7 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
         }
         if (__any_sync(kAll, rescale)) {
           // the stream's earlier P.V must have completed before O is rescaled
-          if (!warp_wait(&pv_done[b], ((i - 2) >> 1) & 1, limit, abort_flag, status, 31)) { ok = false; break; }
+          if (!warp_wait(&pv_done[(i - 2) % LAT], ((i - 2) / LAT) & 1, limit, abort_flag, status, 31)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < 8; ++c) {
@@ -565,13 +602,14 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
       if (!warp_wait(q_ready, n_seg & 1, limit, abort_flag, status, 36)) { ok = false; break; }
       ml[b * 128 + row] = make_float2(M, l);
       warp_arrive(ml_bar);
-      // each stream's last P.V (a stream without a tile in the segment has M = -inf)
+      if (!warp_wait(ml_bar, n_seg & 1, limit, abort_flag, status, 34)) { ok = false; break; }
+      // Each stream's last P.V (a stream without a tile in the segment has M = -inf).
       const int last = it - 1;
       for (int c = 0; c < 2 && ok; ++c) {
         const int i = last - c;
-        if (c < seg.n) ok = warp_wait(&pv_done[i & 1], (i >> 1) & 1, limit, abort_flag, status, 32);
+        if (c < seg.n) ok = warp_wait(&pv_done[i % LAT], (i / LAT) & 1, limit, abort_flag, status, 32);
       }
-      if (!ok || !warp_wait(ml_bar, n_seg & 1, limit, abort_flag, status, 34)) { ok = false; break; }
+      if (!ok) break;
       tc_fence_after();
       if (live_warp) {
         const float2 ml0 = ml[row], ml1 = ml[128 + row];
