@@ -172,8 +172,10 @@ def _check(status: int) -> None:
 
 def _stream_handle(stream) -> int:
     if stream is None:
+        # the handle that torch.cuda.current_stream().cuda_stream gives, without its 5 us of
+        # Python objects (more than the smallest of these kernels takes)
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 

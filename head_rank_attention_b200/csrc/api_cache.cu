@@ -66,6 +66,8 @@ hra_status check_cache(const CacheView& c) {
     return fail(HRA_ERR_INVALID_ARG, "ckv_stride=%lld must be >= d_c=%d and a multiple of %d", c.ckv_stride, c.d_c, byte ? 16 : 8);
   if (c.krope_stride < 64 || c.krope_stride % 8 != 0)
     return fail(HRA_ERR_INVALID_ARG, "krope_stride=%lld must be >= 64 and a multiple of 8", c.krope_stride);
+  if (c.ckv_stride > INT_MAX || c.krope_stride > INT_MAX || c.scale_stride > INT_MAX)
+    return fail(HRA_ERR_UNSUPPORTED, "row strides must be below 2^31");
   if (c.cache_rows < 1 || c.cache_rows > INT_MAX)
     return fail(HRA_ERR_INVALID_ARG, "cache_rows=%lld out of range [1, 2^31-1]", c.cache_rows);
   if (!byte) {
@@ -160,6 +162,8 @@ hra_status run_append(const hra_append_params* p, cudaStream_t stream) {
     return fail(HRA_ERR_INVALID_ARG, "latent_stride=%lld must be >= d_c=%d and a multiple of 8", (long long)p->latent_stride, p->d_c);
   if (p->krope_in_stride < 64 || p->krope_in_stride % 8 != 0)
     return fail(HRA_ERR_INVALID_ARG, "krope_in_stride=%lld must be >= 64 and a multiple of 8", (long long)p->krope_in_stride);
+  if (p->latent_stride > INT_MAX || p->krope_in_stride > INT_MAX || (p->rows_out != nullptr && p->rows_out_stride > INT_MAX))
+    return fail(HRA_ERR_UNSUPPORTED, "row strides must be below 2^31");
   if (p->rows_out != nullptr) {
     if (!aligned(p->rows_out, 16)) return fail(HRA_ERR_INVALID_ARG, "rows_out is not 16-byte aligned");
     if (p->rows_out_stride < p->d_c + 64 || p->rows_out_stride % 8 != 0)
@@ -169,23 +173,24 @@ hra_status run_append(const hra_append_params* p, cudaStream_t stream) {
   hra::AppendArgs a{};
   a.latent = p->latent;
   a.krope_in = p->krope_in;
-  a.latent_stride = p->latent_stride;
-  a.krope_in_stride = p->krope_in_stride;
+  a.latent_stride = static_cast<int>(p->latent_stride);
+  a.krope_in_stride = static_cast<int>(p->krope_in_stride);
   a.slots = p->slots;
   a.positions = p->positions;
   a.ckv = p->ckv;
   a.krope = p->krope;
-  a.ckv_stride = p->ckv_stride;
-  a.krope_stride = p->krope_stride;
+  a.ckv_stride = static_cast<int>(p->ckv_stride);
+  a.krope_stride = static_cast<int>(p->krope_stride);
   a.cache_rows = p->cache_rows;
   a.scale = p->ckv_scale;
-  a.scale_stride = p->ckv_scale_stride;
+  a.scale_stride = static_cast<int>(p->ckv_scale_stride);
   a.rows_out = p->rows_out;
-  a.rows_out_stride = p->rows_out_stride;
+  a.rows_out_stride = static_cast<int>(p->rows_out_stride);
   a.log2_theta = std::log2(static_cast<double>(p->rope_theta));
   a.n_tokens = p->n_tokens;
   a.d_c = p->d_c;
   a.scale_block = p->scale_block > 1 ? p->scale_block : 1;
+  a.block_of = hra::RowDivisor(a.scale_block);
   return done(hra::launch_cache_append(format_of(p->cache_dtype), a, stream), "cache_append launch");
 }
 
@@ -210,21 +215,22 @@ hra_status run_load(const hra_load_params* p, cudaStream_t stream) {
   }
   if (p->out_stride < p->d_c + 64 || p->out_stride % 8 != 0)
     return fail(HRA_ERR_INVALID_ARG, "out_stride=%lld must be >= d_c + 64 and a multiple of 8", (long long)p->out_stride);
+  if (p->out_stride > INT_MAX) return fail(HRA_ERR_UNSUPPORTED, "row strides must be below 2^31");
   if (p->out_seq_stride < 0 || p->out_seq_stride % 8 != 0)
     return fail(HRA_ERR_INVALID_ARG, "out_seq_stride=%lld must be >= 0 and a multiple of 8", (long long)p->out_seq_stride);
   hra::LoadArgs a{};
   a.ckv = p->ckv;
   a.krope = p->krope;
-  a.ckv_stride = p->ckv_stride;
-  a.krope_stride = p->krope_stride;
+  a.ckv_stride = static_cast<int>(p->ckv_stride);
+  a.krope_stride = static_cast<int>(p->krope_stride);
   a.cache_rows = p->cache_rows;
   a.scale = p->ckv_scale;
-  a.scale_stride = p->ckv_scale_stride;
+  a.scale_stride = static_cast<int>(p->ckv_scale_stride);
   a.seq_lens = p->seq_lens;
   a.block_table = p->block_table;
   a.seq_stride = p->seq_stride;
   a.out = p->out;
-  a.out_stride = p->out_stride;
+  a.out_stride = static_cast<int>(p->out_stride);
   a.out_seq_stride = p->out_seq_stride;
   a.batch = p->batch;
   a.max_tokens = p->max_tokens;

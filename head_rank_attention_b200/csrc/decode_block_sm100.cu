@@ -148,14 +148,6 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-  uint64_t r;
-  asm("mul.rn.ftz.f32x2 %0, %1, %2;"
-      : "=l"(r)
-      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
-  return *reinterpret_cast<float2*>(&r);
-}
-
 // Four codes (one word) times a power of two -> four fp16, exactly.
 template <bool E4M3>
 __device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 mul, __half2 bias) {

@@ -25,6 +25,9 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 
+// An element's place, past 32 bits in a long cache.
+__device__ __forceinline__ long long wide(int row, int stride) { return static_cast<long long>(row) * stride; }
+
 // ---------------------------------------------------------------------------- page plan
 constexpr int kPlanThreads = 1024;  // one per sequence (kMaxBatch)
 constexpr int kPlanCluster = 8;
@@ -186,39 +189,40 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
 
 // ------------------------------------------------------------------------------- append
 constexpr int kAppendThreads = 256;
-constexpr int kShortRun = 8;  // rows of a run that one warp holds in registers
+constexpr int kAppendWarps = kAppendThreads / 32;
+constexpr int kShortRun = 8;   // rows of a run that one warp takes by itself
+constexpr int kMaxWindow = 32;  // bits of a word
+constexpr int kMaxScaleBlock = 1024;
 
-__device__ __forceinline__ uint32_t abs_max_bits(uint32_t m, uint32_t bf16x2) {
-  const uint32_t lo = (bf16x2 << 16) & 0x7FFFFFFFu, hi = bf16x2 & 0x7FFF0000u;
-  return max(m, max(lo, hi));
+// Largest magnitude of eight bf16, kept as the bits of |x| in pairs (their unsigned 16-bit order is
+// that of the values, Inf and NaN on top).
+__device__ __forceinline__ uint32_t abs_max2(uint32_t m, uint4 v) {
+  constexpr uint32_t kMag = 0x7FFF7FFFu;
+  return __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & kMag, v.y & kMag), __vmaxu2(v.z & kMag, v.w & kMag)));
 }
-__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
-
-// Four columns of one row: codes to the cache, values to rows_out.
+// The larger of a pair's, over the warp, as fp32 bits.
+__device__ __forceinline__ uint32_t warp_abs_max(uint32_t m2) {
+  return __reduce_max_sync(kAll, max(m2 << 16, m2 & 0xFFFF0000u));
+}
+// The scale of a block whose rows before `first` are kept: the larger of its old one and the
+// new rows'; a scale that is no number stays one.
 template <CacheFormat F>
-__device__ __forceinline__ uint32_t quantize4(uint2 v, float s, float* values) {
-  const float x[4] = {bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y)};
-  uint32_t w = 0;
-#pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const uint32_t c = s > 0.f || s != s ? to_code<F>(code_quotient<F>(x[u], s)) : 0u;
-    values[u] = code_value<F>(c) * s;
-    w |= c << (8 * u);
-  }
-  return w;
+__device__ __forceinline__ float grown_scale(uint32_t amax_bits, float s_old) {
+  const float s = block_scale<F>(amax_bits);
+  return !(s > s_old) && s == s ? s_old : s;
 }
 
 // Rows [0, rows) of a block brought from its old scale to its new one, by `n` threads of
 // which this one is `me`; a thread takes four columns of a row at a time.
 template <CacheFormat F>
-__device__ __forceinline__ void rescale_rows(uint8_t* block, long long stride, int rows, float s_old, float s_new, int me,
+__device__ __forceinline__ void rescale_rows(uint8_t* block, int stride, int rows, float s_old, float s_new, int me,
                                              int n) {
+#pragma unroll 1
   for (int e = me; e < rows * 32; e += n) {
-    uint32_t* p = reinterpret_cast<uint32_t*>(block + (e >> 5) * stride) + (e & 31);
+    uint32_t* p = reinterpret_cast<uint32_t*>(block + wide(e >> 5, stride)) + (e & 31);
     const uint32_t w = *p;
     uint32_t r = 0;
-#pragma unroll
+#pragma unroll 1
     for (int u = 0; u < 4; ++u) r |= rescale_code<F>((w >> (8 * u)) & 0xFFu, s_old, s_new) << (8 * u);
     *p = r;
   }
@@ -229,153 +233,205 @@ __device__ __forceinline__ void rescale_rows(uint8_t* block, long long stride, i
 // Tokens that follow one another in the call and lie in one scale block are a run; the run
 // belongs to the window that holds its first token, whatever windows it reaches into.  A
 // warp takes a run of up to kShortRun rows by itself (a decode step's runs are one row);
-// the block takes longer ones together.  No run needs another's result, so no block waits
-// for another.
+// the block takes longer ones together, and holds the first 64 rows in registers between
+// the maximum and the codes.  A lane has 8 columns, a warp two rows at a time.  No run needs
+// another's result, so no block waits for another.
 template <CacheFormat F>
-__global__ void __launch_bounds__(kAppendThreads) cache_append_kernel(const AppendArgs a, int W) {
+__global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const AppendArgs a, int W) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = blockIdx.y, groups = a.d_c / 128;
-  const int i0 = blockIdx.x * W, i1 = min(i0 + W, a.n_tokens);
+  const int i0 = blockIdx.x * W, n_win = min(W, a.n_tokens - i0);
   const int rows = static_cast<int>(a.cache_rows);
   grid_dep_launch();
   grid_dep_wait();
-  const __nv_bfloat16* latent = static_cast<const __nv_bfloat16*>(a.latent);
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.rows_out);
 
   if (g == groups) {
     // RoPE keys: lane j turns the pair (j, j + 32) by pos * theta^(-2j/64).  The angle is
     // carried in turns in fp64 (positions pass 2^20); its fraction is exact.
-    const double turns = exp2(-2.0 * lane / 64.0 * a.log2_theta) * 0.15915494309189535;
-    const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(a.krope_in);
-    for (int i = i0 + warp; i < i1; i += kAppendThreads / 32) {
-      const int slot = a.slots[i];
-      if (slot < 0 || slot >= rows) continue;
-      const float x1 = __bfloat162float(in[i * a.krope_in_stride + lane]);
-      const float x2 = __bfloat162float(in[i * a.krope_in_stride + 32 + lane]);
-      const double x = a.positions[i] * turns;
+    constexpr int T = kMaxWindow / kAppendWarps;  // tokens of a warp, all loaded before any is used
+    const __nv_bfloat16* in = static_cast<const __nv_bfloat16*>(a.krope_in) + lane;
+    int slot[T], pos[T];
+    float x1[T], x2[T];
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+      const int i = i0 + warp + kAppendWarps * k;
+      const bool on = warp + kAppendWarps * k < n_win;
+      slot[k] = on ? a.slots[i] : -1;
+      pos[k] = on ? a.positions[i] : 0;
+      x1[k] = on ? __bfloat162float(in[wide(i, a.krope_in_stride)]) : 0.f;
+      x2[k] = on ? __bfloat162float(in[wide(i, a.krope_in_stride) + 32]) : 0.f;
+    }
+    __shared__ double turns_s[32];
+    if (warp == 0) turns_s[lane] = exp2(-2.0 * lane / 64.0 * a.log2_theta) * 0.15915494309189535;
+    __syncthreads();
+    const double turns = turns_s[lane];
+#pragma unroll
+    for (int k = 0; k < T; ++k) {
+      if (slot[k] < 0 || slot[k] >= rows) continue;
+      const double x = pos[k] * turns;
       float sn, cs;
       sincospif(2.f * static_cast<float>(x - rint(x)), &sn, &cs);
-      const __nv_bfloat16 y1 = __float2bfloat16_rn(fmaf(x1, cs, -x2 * sn));
-      const __nv_bfloat16 y2 = __float2bfloat16_rn(fmaf(x1, sn, x2 * cs));
-      __nv_bfloat16* k = static_cast<__nv_bfloat16*>(a.krope) + slot * a.krope_stride;
-      k[lane] = y1;
-      k[32 + lane] = y2;
+      const __nv_bfloat16 y1 = __float2bfloat16_rn(fmaf(x1[k], cs, -x2[k] * sn));
+      const __nv_bfloat16 y2 = __float2bfloat16_rn(fmaf(x1[k], sn, x2[k] * cs));
+      __nv_bfloat16* key = static_cast<__nv_bfloat16*>(a.krope) + wide(slot[k], a.krope_stride) + lane;
+      key[0] = y1;
+      key[32] = y2;
       if (out != nullptr) {
-        out[i * a.rows_out_stride + a.d_c + lane] = y1;
-        out[i * a.rows_out_stride + a.d_c + 32 + lane] = y2;
+        __nv_bfloat16* o = out + wide(i0 + warp + kAppendWarps * k, a.rows_out_stride) + a.d_c + lane;
+        o[0] = y1;
+        o[32] = y2;
       }
     }
     return;
   }
 
+  const int half = lane >> 4;  // of the warp's two rows
+  const int col = 128 * g + 8 * (lane & 15);
+  const __nv_bfloat16* latent = static_cast<const __nv_bfloat16*>(a.latent) + col;
+  if (out != nullptr) out += col;
   if constexpr (F == kCacheBf16) {
-    for (int i = i0 + warp; i < i1; i += kAppendThreads / 32) {
-      const int slot = a.slots[i];
+    for (int w = 2 * warp + half; w < n_win; w += 2 * kAppendWarps) {
+      const int i = i0 + w, slot = a.slots[i];
       if (slot < 0 || slot >= rows) continue;
-      const uint2 v = *reinterpret_cast<const uint2*>(latent + i * a.latent_stride + 128 * g + 4 * lane);
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.ckv) + slot * a.ckv_stride + 128 * g + 4 * lane) = v;
-      if (out != nullptr) *reinterpret_cast<uint2*>(out + i * a.rows_out_stride + 128 * g + 4 * lane) = v;
+      const uint4 v = *reinterpret_cast<const uint4*>(latent + wide(i, a.latent_stride));
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.ckv) + wide(slot, a.ckv_stride) + col) = v;
+      if (out != nullptr) *reinterpret_cast<uint4*>(out + wide(i, a.rows_out_stride)) = v;
     }
   } else {
-    __shared__ int long_first[kAppendThreads], n_long;
-    __shared__ uint32_t warp_max[kAppendThreads / 32];
-    if (threadIdx.x == 0) n_long = 0;
-    __syncthreads();
-    uint8_t* ckv = static_cast<uint8_t*>(a.ckv) + 128 * g;
+    // The slots of the window, the token before it and the tokens that a run may reach into:
+    // slot_s[k] is token i0 - 1 + k's, -1 where there is none or it is no row of the cache.  Bit k
+    // of `starts`: token k's scale block is another than the token's before.
+    constexpr int kSee = (1 + kMaxWindow + kMaxScaleBlock + 31) / 32 * 32;
+    __shared__ int slot_s[kSee];
+    __shared__ uint32_t starts[kSee / 32 + 1];
+    __shared__ uint32_t warp_max[kAppendWarps];
     const int blk_rows = a.scale_block;
-    auto block_of = [&](int i) {  // the scale block of token i, or -1
-      if (i < 0 || i >= a.n_tokens) return -1;
-      const int slot = a.slots[i];
-      return slot >= 0 && slot < rows ? slot / blk_rows : -1;
+    const int n_see = 1 + W + blk_rows, words = (n_see + 31) / 32;
+    auto slot_of = [&](int k) {
+      const int i = i0 - 1 + k;
+      const int slot = i >= 0 && i < a.n_tokens ? a.slots[i] : -1;
+      return slot < rows ? max(slot, -1) : -1;
     };
-    for (int i = i0 + warp; i < i1; i += kAppendThreads / 32) {
-      const int blk = block_of(i);
-      if (blk < 0 || block_of(i - 1) == blk) continue;
-      const uint32_t same = __ballot_sync(kAll, block_of(i + lane) == blk);
-      const int len = same == kAll ? 32 : __ffs(~same) - 1;
-      if (len > kShortRun) {
-        if (lane == 0) long_first[atomicAdd(&n_long, 1)] = i;
-        continue;
-      }
-      uint2 v[kShortRun];
-      uint32_t m = 0;
-      int first = blk_rows;
-#pragma unroll
-      for (int r = 0; r < kShortRun; ++r) {
-        if (r >= len) break;
-        v[r] = *reinterpret_cast<const uint2*>(latent + (i + r) * a.latent_stride + 128 * g + 4 * lane);
-        first = min(first, a.slots[i + r] - blk * blk_rows);
-      }
-#pragma unroll
-      for (int r = 0; r < kShortRun; ++r) {
-        if (r >= len) break;
-        m = abs_max_bits(abs_max_bits(m, v[r].x), v[r].y);
-      }
-      m = __reduce_max_sync(kAll, m);
-      float* sp = a.scale + blk * a.scale_stride + g;
-      const float s_old = first > 0 ? *sp : 0.f;
-      float s = block_scale<F>(m);
-      if (!(s > s_old) && s == s) s = s_old;  // a scale that is no number stays one
-      if (first > 0 && s != s_old)
-        rescale_rows<F>(ckv + static_cast<long long>(blk) * blk_rows * a.ckv_stride, a.ckv_stride, first, s_old, s, lane, 32);
-      __syncwarp();
-      if (lane == 0) *sp = s;
-#pragma unroll
-      for (int r = 0; r < kShortRun; ++r) {
-        if (r >= len) break;
-        float val[4];
-        const uint32_t w = quantize4<F>(v[r], s, val);
-        *reinterpret_cast<uint32_t*>(ckv + a.slots[i + r] * a.ckv_stride + 4 * lane) = w;
-        if (out != nullptr)
-          *reinterpret_cast<uint2*>(out + (i + r) * a.rows_out_stride + 128 * g + 4 * lane) =
-              make_uint2(pack_bf16x2(val[0], val[1]), pack_bf16x2(val[2], val[3]));
-      }
+    if (threadIdx.x == 0) starts[words] = 1u;  // the end of what is seen
+    for (int w = warp; w < words; w += kAppendWarps) {
+      const int slot = slot_of(32 * w + lane);
+      const int edge = lane == 0 && w > 0 ? slot_of(32 * w - 1) : -1;
+      const int blk = slot < 0 ? -1 : a.block_of(slot);
+      const int before = __shfl_up_sync(kAll, blk, 1);
+      const uint32_t bits = __ballot_sync(kAll, blk != (lane > 0 ? before : edge < 0 ? -1 : a.block_of(edge)));
+      slot_s[32 * w + lane] = slot;
+      if (lane == 0) starts[w] = bits;
     }
     __syncthreads();
-    for (int k = 0; k < n_long; ++k) {
-      const int i = long_first[k];
-      const int blk = block_of(i);
-      // the run's end, and its first row in the block
-      int len = 0, first = blk_rows;
-      for (;;) {
-        const int mine = i + len + lane;
-        const bool in = block_of(mine) == blk;
-        const uint32_t same = __ballot_sync(kAll, in);
-        if (in && (same == kAll || lane < __ffs(~same) - 1)) first = min(first, a.slots[mine] - blk * blk_rows);
-        if (same != kAll) {
-          len += __ffs(~same) - 1;
-          break;
-        }
-        len += 32;
-      }
-      first = __reduce_min_sync(kAll, first);
+    auto run_length = [&](int k) {  // of the run that starts at k
+      int w = (k + 1) >> 5;
+      uint32_t bits = starts[w] & (0xFFFFFFFFu << ((k + 1) & 31));
+      while (bits == 0) bits = starts[++w];
+      return 32 * w + __ffs(bits) - 1 - k;
+    };
+    uint8_t* ckv = static_cast<uint8_t*>(a.ckv);
+    // The window's runs, a lane looking at each token.
+    const bool run = lane < n_win && (starts[(1 + lane) >> 5] >> ((1 + lane) & 31) & 1u) != 0 && slot_s[1 + lane] >= 0;
+    const int my_len = run ? run_length(1 + lane) : 0;
+    uint32_t long_runs = __ballot_sync(kAll, my_len > kShortRun);
+    uint32_t runs = __ballot_sync(kAll, run) & ~long_runs;
+    for (int turn = 0; runs != 0; runs &= runs - 1, ++turn) {
+      if (turn % kAppendWarps != warp) continue;
+      const int k0 = __ffs(runs);  // the token's place in the list: 1 + its bit
+      const int len = __shfl_sync(kAll, my_len, k0 - 1);
+      const int blk = a.block_of(slot_s[k0]), i = i0 - 1 + k0;
+      const __nv_bfloat16* src = latent + wide(i, a.latent_stride);
+      float* sp = a.scale + wide(blk, a.scale_stride) + g;
+      const float s_was = *sp;  // before the rows: one latency
+      uint4 v[kShortRun / 2];
       uint32_t m = 0;
-      for (int r = warp; r < len; r += kAppendThreads / 32) {
-        const uint2 v = *reinterpret_cast<const uint2*>(latent + (i + r) * a.latent_stride + 128 * g + 4 * lane);
-        m = abs_max_bits(abs_max_bits(m, v.x), v.y);
+#pragma unroll
+      for (int r = 0; r < kShortRun / 2; ++r) {
+        v[r] = make_uint4(0u, 0u, 0u, 0u);
+        if (2 * r + half < len) v[r] = *reinterpret_cast<const uint4*>(src + wide(2 * r + half, a.latent_stride));
       }
-      m = __reduce_max_sync(kAll, m);
+      int first = lane < len ? slot_s[k0 + lane] - blk * blk_rows : blk_rows;
+      first = __reduce_min_sync(kAll, first);  // the run's first row in the block
+#pragma unroll
+      for (int r = 0; r < kShortRun / 2; ++r) m = abs_max2(m, v[r]);
+      m = warp_abs_max(m);
+      const float s_old = first > 0 ? s_was : 0.f;
+      const float s = grown_scale<F>(m, s_old);
+      if (first > 0 && s != s_old)
+        rescale_rows<F>(ckv + 128 * g + wide(blk * blk_rows, a.ckv_stride), a.ckv_stride, first, s_old, s, lane, 32);
+      __syncwarp();
+      if (lane == 0) *sp = s;
+      auto put = [&](int at, uint2 c) {
+        *reinterpret_cast<uint2*>(ckv + wide(slot_s[k0 + at], a.ckv_stride) + col) = c;
+        if (out != nullptr) *reinterpret_cast<uint4*>(out + wide(i + at, a.rows_out_stride)) = dequantize8<F>(c, s);
+      };
+      if (quantize_fast_scale(s)) {
+        const float r_s = 1.f / s;
+#pragma unroll
+        for (int r = 0; r < kShortRun / 2; ++r)
+          if (2 * r + half < len) put(2 * r + half, quantize8_fast<F, kAnyScale>(v[r], s, r_s));
+      } else {
+#pragma unroll 1
+        for (int at = half; at < len; at += 2)
+          put(at, quantize8_exact<F>(*reinterpret_cast<const uint4*>(src + wide(at, a.latent_stride)), s));
+      }
+    }
+    constexpr int HOLD = 4;  // row pairs of a long run that a warp keeps: 8 warps hold 64 rows
+    for (; long_runs != 0; long_runs &= long_runs - 1) {
+      const int k0 = __ffs(long_runs), blk = a.block_of(slot_s[k0]), i = i0 - 1 + k0;
+      const int len = __shfl_sync(kAll, my_len, k0 - 1);
+      const int at0 = 2 * warp + half;
+      const __nv_bfloat16* src = latent + wide(i, a.latent_stride);
+      float* sp = a.scale + wide(blk, a.scale_stride) + g;
+      const float s_was = *sp;
+      uint4 v[HOLD];
+      uint32_t m = 0;
+#pragma unroll
+      for (int r = 0; r < HOLD; ++r) {
+        const int at = at0 + 2 * kAppendWarps * r;
+        v[r] = make_uint4(0u, 0u, 0u, 0u);
+        if (at < len) v[r] = *reinterpret_cast<const uint4*>(src + wide(at, a.latent_stride));
+      }
+      int first = blk_rows;
+      for (int at = lane; at < len; at += 32) first = min(first, slot_s[k0 + at] - blk * blk_rows);
+      first = __reduce_min_sync(kAll, first);
+      const float s_old = first > 0 ? s_was : 0.f;
+#pragma unroll
+      for (int r = 0; r < HOLD; ++r) m = abs_max2(m, v[r]);
+      for (int at = at0 + 2 * kAppendWarps * HOLD; at < len; at += 2 * kAppendWarps)
+        m = abs_max2(m, *reinterpret_cast<const uint4*>(src + wide(at, a.latent_stride)));
+      m = warp_abs_max(m);
       if (lane == 0) warp_max[warp] = m;
-      float* sp = a.scale + blk * a.scale_stride + g;
-      const float s_old = first > 0 ? *sp : 0.f;
       __syncthreads();
 #pragma unroll
-      for (int w = 0; w < kAppendThreads / 32; ++w) m = max(m, warp_max[w]);
-      float s = block_scale<F>(m);
-      if (!(s > s_old) && s == s) s = s_old;
+      for (int w = 0; w < kAppendWarps; ++w) m = max(m, warp_max[w]);
+      const float s = grown_scale<F>(m, s_old);
       if (first > 0 && s != s_old)
-        rescale_rows<F>(ckv + static_cast<long long>(blk) * blk_rows * a.ckv_stride, a.ckv_stride, first, s_old, s,
-                        threadIdx.x, kAppendThreads);
+        rescale_rows<F>(ckv + 128 * g + wide(blk * blk_rows, a.ckv_stride), a.ckv_stride, first, s_old, s, threadIdx.x,
+                        kAppendThreads);
       if (threadIdx.x == 0) *sp = s;
-      for (int r = warp; r < len; r += kAppendThreads / 32) {
-        const uint2 v = *reinterpret_cast<const uint2*>(latent + (i + r) * a.latent_stride + 128 * g + 4 * lane);
-        float val[4];
-        const uint32_t w = quantize4<F>(v, s, val);
-        *reinterpret_cast<uint32_t*>(ckv + a.slots[i + r] * a.ckv_stride + 4 * lane) = w;
-        if (out != nullptr)
-          *reinterpret_cast<uint2*>(out + (i + r) * a.rows_out_stride + 128 * g + 4 * lane) =
-              make_uint2(pack_bf16x2(val[0], val[1]), pack_bf16x2(val[2], val[3]));
+      auto put = [&](int at, uint2 c) {
+        *reinterpret_cast<uint2*>(ckv + wide(slot_s[k0 + at], a.ckv_stride) + col) = c;
+        if (out != nullptr) *reinterpret_cast<uint4*>(out + wide(i + at, a.rows_out_stride)) = dequantize8<F>(c, s);
+      };
+      float r_s = 0.f;
+      const QuantMode mode = quantize_mode<F>(__uint_as_float(m), s, &r_s);
+      int rest = at0;  // rows not in registers, and all of them under scales that need fp64
+      if (quantize_fast_scale(s)) {
+        rest += 2 * kAppendWarps * HOLD;
+        auto put_held = [&](auto quantize) {
+#pragma unroll
+          for (int r = 0; r < HOLD; ++r)
+            if (at0 + 2 * kAppendWarps * r < len) put(at0 + 2 * kAppendWarps * r, quantize(v[r]));
+        };
+        if (mode == kOwnScale) put_held([&](uint4 x) { return quantize8_fast<F, kOwnScale>(x, s, r_s); });
+        else if (mode == kExactScale) put_held([&](uint4 x) { return quantize8_fast<F, kExactScale>(x, s, r_s); });
+        else put_held([&](uint4 x) { return quantize8_fast<F, kAnyScale>(x, s, r_s); });
       }
+#pragma unroll 1
+      for (int at = rest; at < len; at += 2 * kAppendWarps)
+        put(at, quantize8_exact<F>(*reinterpret_cast<const uint4*>(src + wide(at, a.latent_stride)), s));
       __syncthreads();  // warp_max is written again
     }
   }
@@ -405,40 +461,33 @@ __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs
     row_s[threadIdx.x] = row >= 0 && row < a.cache_rows ? static_cast<int>(row) : -1;
   }
   __syncthreads();
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + b * a.out_seq_stride + t0 * a.out_stride;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + b * a.out_seq_stride + wide(t0, a.out_stride);
   constexpr int COLS = F == kCacheBf16 ? 8 : 16;  // columns of one 16-byte load
   const int per_row = a.d_c / COLS;
   for (int e = threadIdx.x; e < n * per_row; e += kLoadThreads) {
     const int r = e / per_row, c = (e % per_row) * COLS;
     const int row = row_s[r];
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    uint4* dst = reinterpret_cast<uint4*>(out + r * a.out_stride + c);
+    uint4* dst = reinterpret_cast<uint4*>(out + wide(r, a.out_stride) + c);
     if constexpr (F == kCacheBf16) {
-      if (row >= 0) v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.ckv) + row * a.ckv_stride + c);
+      if (row >= 0) v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.ckv) + wide(row, a.ckv_stride) + c);
       *dst = v;
     } else {
       float s = 0.f;
       if (row >= 0) {
-        v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.ckv) + row * a.ckv_stride + c);
-        s = a.scale[row / a.scale_block * a.scale_stride + c / 128];
+        v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.ckv) + wide(row, a.ckv_stride) + c);
+        s = a.scale[wide(row / a.scale_block, a.scale_stride) + c / 128];
       }
-      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-      uint32_t o[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        const uint32_t two = w[u >> 1] >> (16 * (u & 1));
-        o[u] = pack_bf16x2(code_value<F>(two & 0xFFu) * s, code_value<F>((two >> 8) & 0xFFu) * s);
-      }
-      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      dst[0] = dequantize8<F>(make_uint2(v.x, v.y), s);
+      dst[1] = dequantize8<F>(make_uint2(v.z, v.w), s);
     }
   }
   for (int e = threadIdx.x; e < n * 8; e += kLoadThreads) {
     const int r = e >> 3, c = (e & 7) * 8;
     const int row = row_s[r];
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (row >= 0) v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.krope) + row * a.krope_stride + c);
-    *reinterpret_cast<uint4*>(out + r * a.out_stride + a.d_c + c) = v;
+    if (row >= 0) v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.krope) + wide(row, a.krope_stride) + c);
+    *reinterpret_cast<uint4*>(out + wide(r, a.out_stride) + a.d_c + c) = v;
   }
 }
 
@@ -449,7 +498,9 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_cache_append(CacheFormat format, const AppendArgs& a, cudaStream_t stream) {
-  const int W = 8;
+  // Windows of 8 tokens, a warp each, while a call can be a decode step (at most kMaxBatch
+  // runs); longer calls are prompts, whose runs the block takes together.
+  const int W = a.n_tokens <= 1024 ? 8 : kMaxWindow;
   const dim3 grid((a.n_tokens + W - 1) / W, a.d_c / 128 + 1);
   auto kern = format == kCacheBf16   ? cache_append_kernel<kCacheBf16>
               : format == kCacheInt8 ? cache_append_kernel<kCacheInt8>

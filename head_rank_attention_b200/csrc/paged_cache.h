@@ -10,6 +10,25 @@ namespace hra {
 // Formats of the cached latent (the RoPE key is bf16 in all of them).
 enum CacheFormat : int { kCacheBf16 = 0, kCacheInt8 = 1, kCacheE4m3 = 2 };
 
+// Division of a row number (below 2^31) by a divisor d of at most 2^20 as a multiplication: with l the bits of
+// d - 1 and m = ceil(2^(31 + l) / d), n / d = n * m >> (31 + l), as m d - 2^(31 + l) < 2^l.
+struct RowDivisor {
+  uint32_t mul = 0;
+  int shift = 0;
+  RowDivisor() = default;
+  explicit RowDivisor(int d) {
+    int l = 0;
+    while ((1 << l) < d) ++l;
+    shift = 31 + l;
+    mul = static_cast<uint32_t>(((uint64_t(1) << shift) + d - 1) / d);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int operator()(int n) const {
+    return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * mul) >> shift);
+  }
+#endif
+};
+
 struct PlanArgs {  // device pointers; see hra_plan_params in hra.h
   const int32_t* seq_lens;
   const int32_t* new_tokens;
@@ -38,32 +57,36 @@ enum PlanStatus : int {
 struct AppendArgs {  // see hra_append_params
   const void* latent;
   const void* krope_in;
-  long long latent_stride, krope_in_stride;  // bf16 elements
+  int latent_stride, krope_in_stride;  // bf16 elements (row strides are below 2^31: an address is one
+                                       //   32 x 32 -> 64-bit multiplication)
   const int32_t* slots;
   const int32_t* positions;
   void* ckv;
   void* krope;
-  long long ckv_stride, krope_stride;  // elements of the cache's types
+  int ckv_stride, krope_stride;  // elements of the cache's types
   long long cache_rows;
   float* scale;
-  long long scale_stride;
+  int scale_stride;
   void* rows_out;  // or nullptr
-  long long rows_out_stride;
+  int rows_out_stride;
   double log2_theta;
   int n_tokens, d_c, scale_block;
+  RowDivisor block_of;  // by scale_block
 };
 
 struct LoadArgs {  // see hra_load_params
   const void* ckv;
   const void* krope;
-  long long ckv_stride, krope_stride, cache_rows;
+  int ckv_stride, krope_stride;
+  long long cache_rows;
   const float* scale;
-  long long scale_stride;
+  int scale_stride;
   const int32_t* seq_lens;
   const int32_t* block_table;  // or nullptr
   long long seq_stride;
   void* out;
-  long long out_stride, out_seq_stride;
+  int out_stride;
+  long long out_seq_stride;
   int batch, max_tokens, d_c, scale_block, max_pages, page_size;
 };
 
