@@ -235,7 +235,7 @@ hra_status run_load(const hra_load_params* p, cudaStream_t stream) {
   a.batch = p->batch;
   a.max_tokens = p->max_tokens;
   a.d_c = p->d_c;
-  a.scale_block = p->scale_block > 1 ? p->scale_block : 1;
+  a.block_of = hra::RowDivisor(p->scale_block > 1 ? p->scale_block : 1);
   a.max_pages = p->max_pages;
   a.page_size = p->page_size;
   return done(hra::launch_cache_load(format_of(p->cache_dtype), a, stream), "cache_load launch");

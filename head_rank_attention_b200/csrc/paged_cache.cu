@@ -5,7 +5,7 @@
 //   entries, the slot (cache row) and position of every new token, and the page pool after
 //   the step.  One request per thread; exclusive prefix sums of the tokens, of the pages
 //   taken and of the pages given back place everything.  A few kilobytes are read and
-//   written: latency bounds it, so it is one launch of one thread-block cluster.
+//   written: latency bounds it, so it is one launch, each block scanning all lengths itself.
 // append: a cache row is the token's latent in the cache's format and its RoPE key turned
 //   by the token's position.  With one scale per block of tokens and 128-wide latent head,
 //   s = max|x| / top over the block; a block that grows token by token keeps the larger of
@@ -17,6 +17,7 @@
 #include "launch.h"
 #include "paged_cache.h"
 #include "quant.cuh"
+#include "schedule.cuh"
 #include "sm100.cuh"
 
 namespace hra {
@@ -29,33 +30,9 @@ constexpr uint32_t kAll = 0xffffffffu;
 __device__ __forceinline__ long long wide(int row, int stride) { return static_cast<long long>(row) * stride; }
 
 // ---------------------------------------------------------------------------- page plan
-constexpr int kPlanThreads = 1024;  // one per sequence (kMaxBatch)
+constexpr int kPlanMinThreads = 128;
+constexpr int kPlanMaxBlocks = 128;
 constexpr int kPlanCluster = 8;
-
-// Exclusive prefix of v over the block's threads, and the total.
-__device__ __forceinline__ unsigned long long block_exclusive(unsigned long long v, unsigned long long* warp_sums,
-                                                              unsigned long long* total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  unsigned long long incl = v;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const unsigned long long u = __shfl_up_sync(kAll, incl, off);
-    if (lane >= off) incl += u;
-  }
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  unsigned long long w = warp_sums[lane];
-  unsigned long long ws = w;
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const unsigned long long u = __shfl_up_sync(kAll, ws, off);
-    if (lane >= off) ws += u;
-  }
-  *total = __shfl_sync(kAll, ws, 31);
-  const unsigned long long before = __shfl_sync(kAll, ws - w, warp);
-  __syncthreads();  // warp_sums may be written again
-  return before + incl - v;
-}
 
 // The sequence that owns item i of an exclusive prefix over B sequences (prefix[B] > i).
 __device__ __forceinline__ int owner(const int* prefix, int B, int i) {
@@ -67,13 +44,18 @@ __device__ __forceinline__ int owner(const int* prefix, int B, int i) {
   return lo;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs a) {
-  __shared__ unsigned long long warp_sums[32];
-  __shared__ int len_s[kPlanThreads], have_s[kPlanThreads];
-  __shared__ int start_s[kPlanThreads + 1], take_s[kPlanThreads + 1], give_s[kPlanThreads + 1];
-  __shared__ int bad_s;  // refusal code << 16 | sequence, the smallest
-  const int t = threadIdx.x, B = a.batch, P = a.page_size;
-  const int rank = blockIdx.x, ranks = gridDim.x;
+// Every block reads all lengths and scans them (one thread for a sequence), and takes its
+// share of the pages and tokens; block 0 writes what there is one of for a sequence.  With
+// CLUSTER the blocks are one cluster and meet before those writes: the outputs may then be
+// the inputs' own buffers.
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) {
+  __shared__ unsigned long long sum_pages[32], sum_tokens[32];
+  __shared__ int len_s[kMaxBatch], have_s[kMaxBatch], start_s[kMaxBatch], take_s[kMaxBatch], give_s[kMaxBatch];
+  __shared__ int bad_s;         // refusal code << 16 | sequence, the smallest
+  __shared__ int ring_s[2];     // the ring's head and tail as places
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = a.batch, P = a.page_size;
+  const int n_warps = blockDim.x >> 5;
   grid_dep_launch();
   grid_dep_wait();
   if (t == 0) bad_s = INT_MAX;
@@ -86,22 +68,48 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
   const int add = gone ? 0 : asked;
   const long long room = static_cast<long long>(a.max_pages) * P;
   const long long after = gone ? 0 : static_cast<long long>(len) + add;
-  if (len < 0 || len > room) atomicMin(&bad_s, kPlanBadLength << 16 | t);
-  else if (after > room) atomicMin(&bad_s, kPlanTableFull << 16 | t);
+  const bool bad_len = len < 0 || len > room, full = !bad_len && after > room;
+  if (bad_len || full) atomicMin(&bad_s, (bad_len ? kPlanBadLength : kPlanTableFull) << 16 | t);
+  // room is below 2^31, so the pages of a good length are
+  const int have = bad_len ? 0 : static_cast<int>((static_cast<long long>(len) + P - 1) / P);
+  const int need = bad_len || full || gone ? 0 : static_cast<int>((after + P - 1) / P) - have;
+  const int freed = gone ? have : 0;
+  // prefix sums of both page counts (batch * max_pages is below 2^31) and of the tokens
+  const unsigned long long my_pages = static_cast<unsigned long long>(freed) << 32 | static_cast<unsigned>(need);
+  unsigned long long pages = my_pages, tokens = static_cast<unsigned>(add);
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const unsigned long long p = __shfl_up_sync(kAll, pages, off), q = __shfl_up_sync(kAll, tokens, off);
+    if (lane >= off) {
+      pages += p;
+      tokens += q;
+    }
+  }
+  if (lane == 31) {
+    sum_pages[warp] = pages;
+    sum_tokens[warp] = tokens;
+  }
+  if (t == 32) ring_s[0] = static_cast<int>(head >= 0 ? head % a.num_pages : 0);
+  if (t == 64) ring_s[1] = static_cast<int>(tail >= 0 ? tail % a.num_pages : 0);
   __syncthreads();
-  int bad = bad_s;
-  const bool sane = bad == INT_MAX;
-  const int have = sane ? static_cast<int>((static_cast<long long>(len) + P - 1) / P) : 0;
-  const int need = sane && !gone ? static_cast<int>((after + P - 1) / P) - have : 0;
-  const int freed = sane && gone ? have : 0;
-  unsigned long long pages_total, tokens_total;
-  const unsigned long long pages =
-      block_exclusive(static_cast<unsigned long long>(freed) << 32 | static_cast<unsigned>(need), warp_sums, &pages_total);
-  const unsigned long long tokens = block_exclusive(add, warp_sums, &tokens_total);
+  unsigned long long wp = lane < n_warps ? sum_pages[lane] : 0, wt = lane < n_warps ? sum_tokens[lane] : 0;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const unsigned long long p = __shfl_up_sync(kAll, wp, off), q = __shfl_up_sync(kAll, wt, off);
+    if (lane >= off) {
+      wp += p;
+      wt += q;
+    }
+  }
+  const unsigned long long pages_total = __shfl_sync(kAll, wp, 31), tokens_total = __shfl_sync(kAll, wt, 31);
+  const unsigned long long pages_before = __shfl_sync(kAll, wp, max(warp - 1, 0));
+  const unsigned long long tokens_before = __shfl_sync(kAll, wt, max(warp - 1, 0));
+  pages += (warp > 0 ? pages_before : 0) - my_pages;
+  tokens += (warp > 0 ? tokens_before : 0) - static_cast<unsigned>(add);
   const int need_total = static_cast<int>(pages_total & 0xFFFFFFFFu), freed_total = static_cast<int>(pages_total >> 32);
   const long long avail = tail - head;
-  int wanted = 0, limit = 0;
-  if (sane) {
+  int bad = bad_s, wanted = 0, limit = 0;
+  if (bad == INT_MAX) {
     if (head < 0 || avail < 0 || avail > a.num_pages || avail + freed_total > a.num_pages) {
       bad = kPlanBadPool << 16;
     } else if (tokens_total > static_cast<unsigned long long>(a.max_tokens)) {
@@ -115,25 +123,23 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
     }
   }
   const bool ok = bad == INT_MAX;
-  // Every block has read the lengths and the free range once all have arrived: the outputs
-  // may be the inputs' own buffers.
-  asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
-  len_s[t] = len;
-  have_s[t] = have;
-  start_s[t] = ok ? static_cast<int>(tokens) : 0;
-  take_s[t] = static_cast<int>(pages & 0xFFFFFFFFu);
-  give_s[t] = static_cast<int>(pages >> 32);
-  if (t == 0) {
-    start_s[kPlanThreads] = ok ? static_cast<int>(tokens_total) : 0;
-    take_s[kPlanThreads] = need_total;
-    give_s[kPlanThreads] = freed_total;
+  const int n_tokens = ok ? static_cast<int>(tokens_total) : 0;
+  if (mine) {
+    len_s[t] = len;
+    have_s[t] = have;
+    start_s[t] = static_cast<int>(tokens);
+    take_s[t] = static_cast<int>(pages & 0xFFFFFFFFu);
+    give_s[t] = static_cast<int>(pages >> 32);
+  }
+  // all lengths and the free range are read once every block (every thread of the one) is here
+  if constexpr (CLUSTER) {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
   }
   __syncthreads();
-  const int n_tokens = start_s[kPlanThreads];
-  if (rank == 0) {
+  if (blockIdx.x == 0) {
     if (mine) {
       a.seq_lens_out[t] = ok ? static_cast<int>(after) : len;
-      a.query_start[t] = start_s[t];
+      a.query_start[t] = ok ? static_cast<int>(tokens) : 0;
     }
     if (t == 0) {
       a.query_start[B] = n_tokens;
@@ -145,24 +151,20 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
       a.status[3] = limit;
     }
   }
-  const int threads = ranks * kPlanThreads, me = rank * kPlanThreads + t;
-  const int head0 = static_cast<int>(head >= 0 ? head % a.num_pages : 0);
-  const int tail0 = static_cast<int>(tail >= 0 ? tail % a.num_pages : 0);
+  const int threads = gridDim.x * blockDim.x, me = blockIdx.x * blockDim.x + t;
+  const int head0 = ring_s[0], tail0 = ring_s[1];
+  auto place = [&](int from, int i) { return from + i < a.num_pages ? from + i : from + i - a.num_pages; };
   if (ok) {
     // pages taken: the ring's next ones, in the order of the sequences
     for (int i = me; i < need_total; i += threads) {
       const int s = owner(take_s, B, i);
-      int at = head0 + i;
-      if (at >= a.num_pages) at -= a.num_pages;
-      a.block_table[static_cast<long long>(s) * a.max_pages + have_s[s] + (i - take_s[s])] = a.free_pages[at];
+      a.block_table[static_cast<long long>(s) * a.max_pages + have_s[s] + (i - take_s[s])] = a.free_pages[place(head0, i)];
     }
     // pages given back: behind the ring's tail.  The ring holds every page at most once, so
     // these places are not among the ones read above.
     for (int i = me; i < freed_total; i += threads) {
       const int s = owner(give_s, B, i);
-      int at = tail0 + i;
-      if (at >= a.num_pages) at -= a.num_pages;
-      a.free_pages[at] = a.block_table[static_cast<long long>(s) * a.max_pages + (i - give_s[s])];
+      a.free_pages[place(tail0, i)] = a.block_table[static_cast<long long>(s) * a.max_pages + (i - give_s[s])];
     }
   }
   for (int i = me; i < a.max_tokens; i += threads) {
@@ -171,14 +173,9 @@ __global__ void __launch_bounds__(kPlanThreads) page_plan_kernel(const PlanArgs 
       const int s = owner(start_s, B, i);
       pos = len_s[s] + (i - start_s[s]);
       const int p = pos / P;
-      int page;
-      if (p < have_s[s]) {
-        page = a.block_table[static_cast<long long>(s) * a.max_pages + p];
-      } else {
-        int at = head0 + take_s[s] + (p - have_s[s]);
-        if (at >= a.num_pages) at -= a.num_pages;
-        page = a.free_pages[at];
-      }
+      // a cached page from the table, a new one from the ring
+      const int page = p < have_s[s] ? a.block_table[static_cast<long long>(s) * a.max_pages + p]
+                                     : a.free_pages[place(head0, take_s[s] + (p - have_s[s]))];
       // a table entry that is no page of the pool has no slot
       slot = page >= 0 && page < a.num_pages ? page * P + (pos - p * P) : -1;
     }
@@ -439,16 +436,18 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const A
 
 // --------------------------------------------------------------------------------- load
 constexpr int kLoadThreads = 256;
-constexpr int kLoadTokens = 32;  // per block
+constexpr int kLoadTokens = 32;  // most of a block
 
-// grid (tokens / kLoadTokens, B).
+// grid (tokens / per_block, B).  A thread has one 16-byte load in flight and its stores: with two
+// or four the long loads were slower (56 to 62 us instead of 53 for 160 k rows), reads and writes
+// coming in longer turns.
 template <CacheFormat F>
-__global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs a) {
+__global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs a, int per_block) {
   __shared__ int row_s[kLoadTokens];
   grid_dep_launch();
   grid_dep_wait();
-  const int b = blockIdx.y, t0 = blockIdx.x * kLoadTokens;
-  const int n = min(min(a.seq_lens[b], a.max_tokens) - t0, kLoadTokens);
+  const int b = blockIdx.y, t0 = blockIdx.x * per_block;
+  const int n = min(min(a.seq_lens[b], a.max_tokens) - t0, per_block);
   if (n <= 0) return;
   if (threadIdx.x < n) {
     const int t = t0 + threadIdx.x;
@@ -463,9 +462,9 @@ __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs
   __syncthreads();
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out) + b * a.out_seq_stride + wide(t0, a.out_stride);
   constexpr int COLS = F == kCacheBf16 ? 8 : 16;  // columns of one 16-byte load
-  const int per_row = a.d_c / COLS;
+  const int per_row = a.d_c / COLS, shift = __ffs(per_row) - 1;
   for (int e = threadIdx.x; e < n * per_row; e += kLoadThreads) {
-    const int r = e / per_row, c = (e % per_row) * COLS;
+    const int r = e >> shift, c = (e & (per_row - 1)) * COLS;
     const int row = row_s[r];
     uint4 v = make_uint4(0u, 0u, 0u, 0u);
     uint4* dst = reinterpret_cast<uint4*>(out + wide(r, a.out_stride) + c);
@@ -476,7 +475,7 @@ __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs
       float s = 0.f;
       if (row >= 0) {
         v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.ckv) + wide(row, a.ckv_stride) + c);
-        s = a.scale[wide(row / a.scale_block, a.scale_stride) + c / 128];
+        s = a.scale[wide(a.block_of(row), a.scale_stride) + c / 128];
       }
       dst[0] = dequantize8<F>(make_uint2(v.x, v.y), s);
       dst[1] = dequantize8<F>(make_uint2(v.z, v.w), s);
@@ -494,7 +493,15 @@ __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs
 }  // namespace
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream) {
-  return launch_kernel_cluster(page_plan_kernel, dim3(kPlanCluster), dim3(kPlanThreads), 0, stream, true, kPlanCluster, a);
+  // A thread for a sequence, and a token or so for a thread: a step of 64 requests is one block of
+  // 128, and 65536 tokens are spread over 64 SMs (11.8 us on one cluster's 8, 6.8 so).
+  // Blocks that read lengths which another block overwrites must meet, in one cluster.
+  const int threads = (a.batch > kPlanMinThreads ? a.batch + 31 : kPlanMinThreads) / 32 * 32;
+  const int blocks = (a.max_tokens + threads - 1) / threads;
+  const bool in_place = a.seq_lens == a.seq_lens_out || a.free_range == a.free_range_out;
+  if (!in_place || blocks == 1)
+    return launch_kernel(page_plan_kernel<false>, dim3(blocks < kPlanMaxBlocks ? blocks : kPlanMaxBlocks), dim3(threads), 0, stream, true, a);
+  return launch_kernel_cluster(page_plan_kernel<true>, dim3(kPlanCluster), dim3(threads), 0, stream, true, kPlanCluster, a);
 }
 
 cudaError_t launch_cache_append(CacheFormat format, const AppendArgs& a, cudaStream_t stream) {
@@ -509,11 +516,14 @@ cudaError_t launch_cache_append(CacheFormat format, const AppendArgs& a, cudaStr
 }
 
 cudaError_t launch_cache_load(CacheFormat format, const LoadArgs& a, cudaStream_t stream) {
-  const dim3 grid((a.max_tokens + kLoadTokens - 1) / kLoadTokens, a.batch);
+  // Blocks of 32 tokens, or of 16 where that leaves SMs idle (2048 tokens: 2.95 instead of 3.46 us;
+  // long loads gain 2 % from the larger).
+  const int per_block = static_cast<long long>((a.max_tokens + kLoadTokens - 1) / kLoadTokens) * a.batch < 2 * 148 ? 16 : kLoadTokens;
+  const dim3 grid((a.max_tokens + per_block - 1) / per_block, a.batch);
   auto kern = format == kCacheBf16   ? cache_load_kernel<kCacheBf16>
               : format == kCacheInt8 ? cache_load_kernel<kCacheInt8>
                                      : cache_load_kernel<kCacheE4m3>;
-  return launch_kernel(kern, grid, dim3(kLoadThreads), 0, stream, true, a);
+  return launch_kernel(kern, grid, dim3(kLoadThreads), 0, stream, true, a, per_block);
 }
 
 }  // namespace hra

@@ -87,7 +87,8 @@ struct LoadArgs {  // see hra_load_params
   void* out;
   int out_stride;
   long long out_seq_stride;
-  int batch, max_tokens, d_c, scale_block, max_pages, page_size;
+  int batch, max_tokens, d_c, max_pages, page_size;
+  RowDivisor block_of;  // by the rows that share a scale
 };
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream);
