@@ -68,7 +68,7 @@ struct BlockCfg {
   static constexpr int WARP_CONV = 8, CONV_WARPS = 3, WARP_PRODUCER = 14, WARP_MMA = 15;
   static constexpr int THREADS = 512;
   // setmaxnreg: 256 softmax threads and 256 others share the 128 * 512 registers of the launch
-  static constexpr int SOFTMAX_REGS = 152, OTHER_REGS = 104;
+  static constexpr int SOFTMAX_REGS = 160, OTHER_REGS = 96;
   static constexpr int QR_BYTES = 128 * 128;
   static constexpr int BAR_BYTES = 512;
   static constexpr int ML_BYTES = 2 * 128 * 8;
@@ -502,18 +502,10 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
       for (int k = 0; k < seg.n; ++k) {
         const int i = it + k;
         if ((i & 1) != b) continue;
-        if (!warp_wait(&qk_done[i % RAW], (i / RAW) & 1, limit, abort_flag, status, 30)) { ok = false; break; }
-        tc_fence_after();
-        if (!live_warp) {  // rows that are no head: their P and O are never read
-          warp_arrive(&p_ready[b]);
-          continue;
-        }
-        // already complete; orders the producer's writes of the chunk parameters (which the
-        // converters have seen) before the reads.  The place of tile i + PAR is written after QK(i + RAW),
-        // which comes after this stream's softmax of tile i + 2.
+        // The chunk parameters, while the scores are on their way: the converters have seen them when
+        // the tile is converted.  The place of tile i + PAR is written after QK(i + RAW), which
+        // comes after this stream's softmax of tile i + 2.
         if (!warp_wait(&conv[i % LAT], (i / LAT) & 1, limit, abort_flag, status, 35)) { ok = false; break; }
-        uint32_t sr[NT];
-        tmem_load<NT>(s_cols, sr);
         float kc[CHUNKS], lam[CHUNKS], inv[CHUNKS];
 #pragma unroll
         for (int c = 0; c < CHUNKS; ++c) {
@@ -522,6 +514,14 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
           lam[c] = p.y;
           inv[c] = p.z;
         }
+        if (!warp_wait(&qk_done[i % RAW], (i / RAW) & 1, limit, abort_flag, status, 30)) { ok = false; break; }
+        tc_fence_after();
+        if (!live_warp) {  // rows that are no head: their P and O are never read
+          warp_arrive(&p_ready[b]);
+          continue;
+        }
+        uint32_t sr[NT];
+        tmem_load<NT>(s_cols, sr);
         tmem_ld_wait();
         const int n_valid = L - (seg.first + k - prefix[s]) * NT;
         if (n_valid < NT) {
