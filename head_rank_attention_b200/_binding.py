@@ -179,6 +179,27 @@ def _stream_handle(stream) -> int:
     return getattr(stream, "cuda_stream", stream)
 
 
+def _on_one_device(p, tensors) -> None:
+    """Remember which device p's tensors are on (they share one)."""
+    devices = {t.device for t in tensors if t is not None}
+    if len(devices) != 1:
+        raise ValueError(f"the tensors lie on several devices: {sorted(map(str, devices))}")
+    p._device = devices.pop()
+
+
+def _launch_stream(p, stream) -> int:
+    """The handle of the stream to launch p on; p's tensors must be on the current device,
+    which is the one that the kernel runs on."""
+    import torch
+    device = getattr(p, "_device", None)
+    if device is not None:
+        if device.type != "cuda":
+            raise ValueError(f"the tensors are on {device}, not on a CUDA device")
+        if device.index != torch.cuda.current_device():
+            raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
+    return _stream_handle(stream)
+
+
 def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
@@ -377,6 +398,8 @@ def make_plan_params(seq_lens, new_tokens, block_table, free_pages, free_range, 
     _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.is_contiguous()
           and int(block_table.shape[0]) == B, f"block_table must be contiguous int32 [{B}, max_pages]")
     p = HraPlanParams()
+    _on_one_device(p, (seq_lens, new_tokens, block_table, free_pages, free_range, seq_lens_out, free_range_out, query_start,
+                       slots, status, positions))
     p.batch, p.page_size, p.max_pages = B, int(page_size), int(block_table.shape[1])
     p.num_pages, p.max_tokens = int(free_pages.shape[0]), int(slots.shape[0])
     p.seq_lens, p.new_tokens, p.block_table = _ptr(seq_lens), _ptr(new_tokens), _ptr(block_table)
@@ -390,11 +413,11 @@ def page_plan(p: HraPlanParams, stream=None) -> None:
     """Plan a step on the device: new block table entries, slots and positions of the new
     tokens, lengths and page pool after the step.  A refused step is seen in p's status
     tensor, or with check_plan_status."""
-    _check(load_library().hra_page_plan(ctypes.byref(p), ctypes.c_void_p(_stream_handle(stream))))
+    _check(load_library().hra_page_plan(ctypes.byref(p), ctypes.c_void_p(_launch_stream(p, stream))))
 
 
 def check_plan_status(p: HraPlanParams, stream=None) -> None:
-    _check(load_library().hra_check_plan_status(ctypes.byref(p), ctypes.c_void_p(_stream_handle(stream))))
+    _check(load_library().hra_check_plan_status(ctypes.byref(p), ctypes.c_void_p(_launch_stream(p, stream))))
 
 
 def _rows_2d(t, cols: int, dtype, name: str) -> None:
@@ -421,6 +444,7 @@ def make_append_params(latent, krope_in, slots, positions, ckv, krope, *, ckv_sc
     optionally rows_out bf16 [n, d_c + 64] for the rows as the cache stands for them."""
     import torch
     p = HraAppendParams()
+    _on_one_device(p, (latent, krope_in, slots, positions, ckv, krope, ckv_scale, rows_out))
     p.n_tokens, p.d_c, p.d_rope = int(latent.shape[0]), int(latent.shape[1]), int(krope_in.shape[1])
     _rows_2d(latent, p.d_c, torch.bfloat16, "latent")
     _rows_2d(krope_in, 64, torch.bfloat16, "krope_in")
@@ -442,7 +466,7 @@ def make_append_params(latent, krope_in, slots, positions, ckv, krope, *, ckv_sc
 def cache_append(p: HraAppendParams, stream=None) -> None:
     """Write new tokens into the cache: latents in the cache's format, RoPE keys turned to
     their positions."""
-    _check(load_library().hra_cache_append(ctypes.byref(p), ctypes.c_void_p(_stream_handle(stream))))
+    _check(load_library().hra_cache_append(ctypes.byref(p), ctypes.c_void_p(_launch_stream(p, stream))))
 
 
 def make_load_params(ckv, krope, seq_lens, out, *, block_table=None, page_size: int = 0, seq_stride: int = 0,
@@ -451,6 +475,7 @@ def make_load_params(ckv, krope, seq_lens, out, *, block_table=None, page_size: 
     cache as make_params takes it, seq_lens int32 [B] and out bf16 [B, max_tokens, d_c + 64]."""
     import torch
     p = HraLoadParams()
+    _on_one_device(p, (ckv, krope, seq_lens, out, block_table, ckv_scale))
     p.batch, p.max_tokens, p.d_c, p.d_rope = int(seq_lens.shape[0]), int(out.shape[1]), int(ckv.shape[1]), 64
     _vector(seq_lens, None, torch.int32, "seq_lens")
     _need(out.dim() == 3 and out.dtype == torch.bfloat16 and out.stride(2) == 1
@@ -470,4 +495,4 @@ def make_load_params(ckv, krope, seq_lens, out, *, block_table=None, page_size: 
 def cache_load(p: HraLoadParams, stream=None) -> None:
     """Read cached rows back as contiguous bf16 rows [C_KV | K_RoPE], the form mlra_prefill
     takes."""
-    _check(load_library().hra_cache_load(ctypes.byref(p), ctypes.c_void_p(_stream_handle(stream))))
+    _check(load_library().hra_cache_load(ctypes.byref(p), ctypes.c_void_p(_launch_stream(p, stream))))

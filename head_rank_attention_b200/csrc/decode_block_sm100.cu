@@ -47,11 +47,11 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 
-// E's range.  The rope key is multiplied by 2^-(E + kRopeShift) at most 2^(-kMinExp - kRopeShift)
-// = 2^6 and the rope query by 2^kRopeShift: keys up to 1000 and queries up to 4000 stay in
-// fp16's range whatever the scales.  Below kMinExp codes are shifted down instead (exact until s =
-// 2^-25); above kMaxExp, up.
-constexpr int kMinExp = -10, kMaxExp = 10, kRopeShift = 4;
+// E's range.  The rope key is multiplied by 1 / sigma 2^-kRopeShift, at most 2^(-kMinExp - kRopeShift)
+// = 2^4, and the rope query by 2^kRopeShift: keys and queries below 4000 stay in fp16's range
+// whatever the scales.  Below kMinExp codes are shifted down instead (exact until s = 2^-23);
+// above kMaxExp, up.
+constexpr int kMinExp = -8, kMaxExp = 10, kRopeShift = 4;
 
 struct BlockCfg {
   static constexpr int NT = 96;
@@ -68,6 +68,7 @@ struct BlockCfg {
   static constexpr int WARP_CONV = 8, CONV_WARPS = 3, WARP_PRODUCER = 14, WARP_MMA = 15;
   static constexpr int THREADS = 512;
   // setmaxnreg: 256 softmax threads and 256 others share the 128 * 512 registers of the launch
+  static constexpr int LAUNCH_REGS = 128;
   static constexpr int SOFTMAX_REGS = 160, OTHER_REGS = 96;
   static constexpr int QR_BYTES = 128 * 128;
   static constexpr int BAR_BYTES = 512;
@@ -75,7 +76,7 @@ struct BlockCfg {
   static constexpr int PAR_BYTES = PAR * CHUNKS * 32;  // ChunkParams
   static constexpr int MISC_BYTES = BAR_BYTES + ML_BYTES + PAR_BYTES + 4 * (kMaxBatch + 1);
   static constexpr int SMEM_BYTES = 1024 + RAW * RAW_BYTES + LAT * LAT_BYTES + QR_BYTES + MISC_BYTES;
-  static_assert((SOFTMAX_REGS + OTHER_REGS) * 256 == 128 * THREADS, "register split");
+  static_assert((SOFTMAX_REGS + OTHER_REGS) * 256 == LAUNCH_REGS * THREADS, "register split");
   static_assert(SMEM_BYTES <= 232448, "shared memory budget");
   static_assert(PAR >= RAW + 4, "chunk parameters");
   // A team waits only for its own tiles' copies, and copies may land out of order: were a stage
@@ -652,6 +653,14 @@ cudaError_t launch_decode_block_kernel(const CUtensorMap& map_ckv, const CUtenso
                                        int groups, cudaStream_t stream, bool pdl) {
   using C = BlockCfg;
   auto kern = a.cache_int8 == 2 ? decode_block_kernel<true> : decode_block_kernel<false>;
+  // The softmax warps' setmaxnreg waits for registers that a launch with fewer would not have.
+  static const bool regs_ok = [] {
+    cudaFuncAttributes i8{}, f8{};
+    return cudaFuncGetAttributes(&i8, decode_block_kernel<false>) == cudaSuccess &&
+           cudaFuncGetAttributes(&f8, decode_block_kernel<true>) == cudaSuccess && i8.numRegs == C::LAUNCH_REGS &&
+           f8.numRegs == C::LAUNCH_REGS;
+  }();
+  if (!regs_ok) return cudaErrorInvalidKernelImage;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(a.d_c / 128, groups), dim3(C::THREADS), C::SMEM_BYTES, stream, pdl, map_ckv,

@@ -171,7 +171,9 @@ typedef struct {
      contiguous layout seq_stride (batch > 1); cache_dtype is HRA_INT8 or HRA_E4M3.  The cache
      then holds d_c + 2 * d_rope bytes per token.  A scale is finite and >= 0 (a scale that is no
      number makes the output of the sequences that read it no number); the values it
-     stands for, |code * scale|, stay below 65504.  hra_cache_append writes this format.        */
+     stands for, |code * scale|, stay below 65504; |krope| and the query's |q_rope| stay below
+     4000.  Scales differ freely from block to block; a value is resolved to 2^-32.  ckv_scale has
+     one row for each begun block of cache_rows.  hra_cache_append writes this format.            */
   int scale_block;
 } hra_decode_params;
 
@@ -322,7 +324,8 @@ HRA_API hra_status hra_check_plan_status(const hra_plan_params* p, void* stream)
  * rows_out (optional): what the cache now stands for, bf16 [n_tokens, d_c + 64] (latent rounded to
  * bf16, turned RoPE key), the rows that mlra_prefill reads; rows of skipped tokens are left.
  * d_c in {128, 256, 512}, d_rope = 64; 1 <= n_tokens < 2^31.  latent, krope_in, ckv, krope and
- * rows_out 16-byte aligned, bf16 strides multiples of 8, 8-bit ones of 16.  One launch, no workspace.
+ * rows_out 16-byte aligned, bf16 strides multiples of 8, 8-bit ones of 16, all below 2^31.  No two buffers
+ * overlap.  One launch, no workspace.
  */
 typedef struct {
   int n_tokens, d_c, d_rope;

@@ -195,6 +195,36 @@ def test_empty_sequences_and_bf16_out():
     assert max_rel <= MAX_REL and mean_rel <= MEAN_REL + 2.0 ** -8 / 2  # a uniform rounding averages half of its bound
 
 
+def test_all_sequences_empty():
+    wl = _case("none", (64, 64), page_size=64)
+    inp = synth.make_inputs(wl)
+    codes, scale = _quantize(inp.cache[:, :512], 64, "int8")
+    inp.seq_lens[:] = 0
+    assert (_run(inp, wl, codes, scale, 64) == 0).all()
+
+
+def test_largest_batch():
+    """1024 sequences of 1 to 130 tokens, few heads."""
+    r = np.random.default_rng(9)
+    wl = _case("b1024", tuple(int(n) for n in r.integers(1, 131, 1024)), heads=4, page_size=32)
+    inp = synth.make_inputs(wl)
+    codes, scale = _quantize(inp.cache[:, :512], 32, "e4m3")
+    assert_parity(_run(inp, wl, codes, scale, 32), _oracle(inp, wl, codes, scale, 32), "1024 sequences")
+
+
+def test_large_rope_keys_and_queries():
+    """RoPE keys in the hundreds against small latents, and the reverse: the one divided by the
+    tile's scale, the other times it, within fp16."""
+    wl = _case("rope", (500, 97), page_size=64)
+    for k_size, q_size, c_size in ((500.0, 2.0 ** -9, 2.0 ** -7), (2.0 ** -6, 4.0, 2.0 ** 4), (3000.0, 2.0 ** -12, 2.0 ** -9)):
+        inp = synth.make_inputs(wl)
+        inp.cache[:, 512:] = (inp.cache[:, 512:].float() / 4.5 * k_size).to(torch.bfloat16)
+        inp.cache[:, :512] = (inp.cache[:, :512].float() * c_size).to(torch.bfloat16)
+        inp.q[..., 128:] = (inp.q[..., 128:].float() * q_size).to(torch.bfloat16)
+        codes, scale = _quantize(inp.cache[:, :512], 64, "int8")
+        assert_parity(_run(inp, wl, codes, scale, 64), _oracle(inp, wl, codes, scale, 64), f"{k_size} {q_size} {c_size}")
+
+
 def test_a_scale_that_is_no_number_stays_in_its_sequence():
     wl = _case("nan", (300, 300), page_size=64)
     inp = synth.make_inputs(wl)

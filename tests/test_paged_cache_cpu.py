@@ -256,3 +256,18 @@ def test_binding_checks_tensors():
                 dict(seq_lens=torch.zeros(2, dtype=torch.int64))):
         with pytest.raises(ValueError):
             hra.make_load_params(**{**ld, **bad})
+
+
+def test_launches_need_their_tensors_on_the_current_device():
+    """Tensors in host memory, or on several devices, are refused before any launch."""
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
+    bf = lambda *n: torch.zeros(*n, dtype=torch.bfloat16)  # noqa: E731
+    i64 = torch.zeros(2, dtype=torch.int64)
+    plan = hra.make_plan_params(i32(2), i32(2), i32(2, 4), i32(8), i64, i32(2), i64.clone(), i32(3), i32(5), i32(4), page_size=64)
+    put = hra.make_append_params(bf(5, 128), bf(5, 64), i32(5), i32(5), bf(64, 128), bf(64, 64))
+    load = hra.make_load_params(bf(64, 128), bf(64, 64), i32(1), bf(1, 7, 192), seq_stride=64)
+    for call, p in ((hra.page_plan, plan), (hra.check_plan_status, plan), (hra.cache_append, put), (hra.cache_load, load)):
+        with pytest.raises(ValueError, match="not on a CUDA device"):
+            call(p)
+    with pytest.raises(ValueError, match="several devices"):
+        hra.make_append_params(bf(5, 128), bf(5, 64), i32(5), i32(5), bf(64, 128).to("meta"), bf(64, 64))

@@ -323,6 +323,31 @@ def test_load(fmt, block, d_c, page):
         assert (got[b, m:] == 7.0).all() and (got[b, :, d_c + 64:] == 7.0).all()
 
 
+@pytest.mark.parametrize("fmt", ["int8", "bf16"])
+def test_offsets_past_32_bits(fmt):
+    """Append and load at the end of a cache of more than 2^31 bytes (and, for bf16, elements)."""
+    rows = (4_400_000 // 64) * 64
+    ckv = torch.zeros(rows, 512, dtype=DTYPE[fmt], device="cuda")
+    krope = torch.zeros(rows, 64, dtype=torch.bfloat16, device="cuda")
+    scale = torch.zeros(rows // 64, 4, device="cuda") if fmt == "int8" else None
+    block = 64 if fmt == "int8" else 0
+    r = np.random.default_rng(2)
+    x = torch.tensor(r.standard_normal((70, 576)), dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(rows - 70, rows, dtype=torch.int32, device="cuda")
+    seen = torch.zeros(70, 576, dtype=torch.bfloat16, device="cuda")
+    hra.cache_append(hra.make_append_params(x[:, :512], x[:, 512:], slots, slots, ckv, krope, ckv_scale=scale, scale_block=block,
+                                            rows_out=seen))
+    page = rows // 64
+    table = torch.tensor([[page - 2, page - 1]], dtype=torch.int32, device="cuda")
+    out = torch.zeros(1, 128, 576, dtype=torch.bfloat16, device="cuda")
+    hra.cache_load(hra.make_load_params(ckv, krope, torch.tensor([128], dtype=torch.int32, device="cuda"), out, block_table=table,
+                                        page_size=64, ckv_scale=scale, scale_block=block))
+    assert torch.equal(out[0, 58:], seen) and (out[0, :58] == 0).all()
+    assert int((ckv[:rows - 70].view(torch.int8) != 0).sum()) == 0
+    if fmt == "bf16":
+        assert torch.equal(seen[:, :512], x[:, :512])
+
+
 def test_load_pages_outside_the_cache_are_zero():
     r = np.random.default_rng(1)
     codes, scale, krope = _random_cache(r, 128, 128, 32, "int8")
