@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWarps = kAppendThreads / 32;
 constexpr int kShortRun = 8;   // rows of a run that one warp takes by itself
-constexpr int kMaxWindow = 32;  // bits of a word
+constexpr int kMaxWindow = 64;
 constexpr int kMaxScaleBlock = 1024;
 
 // Largest magnitude of eight bf16, kept as the bits of |x| in pairs (their unsigned 16-bit order is
@@ -353,15 +353,24 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const A
       return 32 * w + __ffs(bits) - 1 - k;
     };
     uint8_t* ckv = static_cast<uint8_t*>(a.ckv);
-    // The window's runs, a lane looking at each token.
-    const bool run = lane < n_win && (starts[(1 + lane) >> 5] >> ((1 + lane) & 31) & 1u) != 0 && slot_s[1 + lane] >= 0;
-    const int my_len = run ? run_length(1 + lane) : 0;
-    uint32_t long_runs = __ballot_sync(kAll, my_len > kShortRun);
-    uint32_t runs = __ballot_sync(kAll, run) & ~long_runs;
+    // The window's runs, a lane looking at two tokens.
+    int my_len[2] = {0, 0};
+    unsigned long long runs = 0, long_runs = 0;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (32 * h >= W) break;
+      const int w = 32 * h + lane;
+      const bool run = w < n_win && (starts[(1 + w) >> 5] >> ((1 + w) & 31) & 1u) != 0 && slot_s[1 + w] >= 0;
+      my_len[h] = run ? run_length(1 + w) : 0;
+      runs |= static_cast<unsigned long long>(__ballot_sync(kAll, run)) << (32 * h);
+      long_runs |= static_cast<unsigned long long>(__ballot_sync(kAll, my_len[h] > kShortRun)) << (32 * h);
+    }
+    auto length_of = [&](int k0) { return __shfl_sync(kAll, k0 > 32 ? my_len[1] : my_len[0], (k0 - 1) & 31); };
+    runs &= ~long_runs;
     for (int turn = 0; runs != 0; runs &= runs - 1, ++turn) {
       if (turn % kAppendWarps != warp) continue;
-      const int k0 = __ffs(runs);  // the token's place in the list: 1 + its bit
-      const int len = __shfl_sync(kAll, my_len, k0 - 1);
+      const int k0 = __ffsll(runs);  // the token's place in the list: 1 + its bit
+      const int len = length_of(k0);
       const int blk = a.block_of(slot_s[k0]), i = i0 - 1 + k0;
       const __nv_bfloat16* src = latent + wide(i, a.latent_stride);
       float* sp = a.scale + wide(blk, a.scale_stride) + g;
@@ -401,8 +410,8 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const A
     }
     constexpr int HOLD = 4;  // row pairs of a long run that a warp keeps: 8 warps hold 64 rows
     for (; long_runs != 0; long_runs &= long_runs - 1) {
-      const int k0 = __ffs(long_runs), blk = a.block_of(slot_s[k0]), i = i0 - 1 + k0;
-      const int len = __shfl_sync(kAll, my_len, k0 - 1);
+      const int k0 = __ffsll(long_runs), blk = a.block_of(slot_s[k0]), i = i0 - 1 + k0;
+      const int len = length_of(k0);
       const int at0 = 2 * warp + half;
       const __nv_bfloat16* src = latent + wide(i, a.latent_stride);
       float* sp = a.scale + wide(blk, a.scale_stride) + g;
@@ -531,8 +540,9 @@ cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_cache_append(CacheFormat format, const AppendArgs& a, cudaStream_t stream) {
   // Windows of 8 tokens, a warp each, while a call can be a decode step (at most kMaxBatch
-  // runs); longer calls are prompts, whose runs the block takes together.
-  const int W = a.n_tokens <= 1024 ? 8 : kMaxWindow;
+  // runs); longer calls are prompts, whose runs the block takes together: a window of a block's
+  // length has one, more or less.
+  const int W = a.n_tokens <= kMaxBatch ? 8 : a.scale_block >= kMaxWindow ? kMaxWindow : 32;
   const dim3 grid((a.n_tokens + W - 1) / W, a.d_c / 128 + 1);
   auto kern = format == kCacheBf16   ? cache_append_kernel<kCacheBf16>
               : format == kCacheInt8 ? cache_append_kernel<kCacheInt8>
