@@ -187,17 +187,17 @@ def _on_one_device(p, tensors) -> None:
     p._device = devices.pop()
 
 
-def _launch_stream(p, stream) -> int:
-    """The handle of the stream to launch p on; p's tensors must be on the current device,
-    which is the one that the kernel runs on."""
+def _launch(name: str, p, stream) -> None:
+    """Call an entry point with p on a stream (the current one by default).  p's tensors must be
+    on the current device, which is the one that the kernel runs on."""
     import torch
-    device = getattr(p, "_device", None)
-    if device is not None:
-        if device.type != "cuda":
-            raise ValueError(f"the tensors are on {device}, not on a CUDA device")
-        if device.index != torch.cuda.current_device():
-            raise ValueError(f"the tensors are on {device}, the current device is cuda:{torch.cuda.current_device()}")
-    return _stream_handle(stream)
+    device = p._device
+    current = torch.cuda.current_device() if device.type == "cuda" else None
+    if device.index != current or current is None:
+        raise ValueError(f"the tensors are on {device}, "
+                         + ("not on a CUDA device" if current is None else f"the current device is cuda:{current}"))
+    handle = torch._C._cuda_getCurrentRawStream(current) if stream is None else getattr(stream, "cuda_stream", stream)
+    _check(getattr(load_library(), name)(ctypes.byref(p), handle))
 
 
 def _ptr(t) -> int:
@@ -413,11 +413,11 @@ def page_plan(p: HraPlanParams, stream=None) -> None:
     """Plan a step on the device: new block table entries, slots and positions of the new
     tokens, lengths and page pool after the step.  A refused step is seen in p's status
     tensor, or with check_plan_status."""
-    _check(load_library().hra_page_plan(ctypes.byref(p), ctypes.c_void_p(_launch_stream(p, stream))))
+    _launch("hra_page_plan", p, stream)
 
 
 def check_plan_status(p: HraPlanParams, stream=None) -> None:
-    _check(load_library().hra_check_plan_status(ctypes.byref(p), ctypes.c_void_p(_launch_stream(p, stream))))
+    _launch("hra_check_plan_status", p, stream)
 
 
 def _rows_2d(t, cols: int, dtype, name: str) -> None:
@@ -466,7 +466,7 @@ def make_append_params(latent, krope_in, slots, positions, ckv, krope, *, ckv_sc
 def cache_append(p: HraAppendParams, stream=None) -> None:
     """Write new tokens into the cache: latents in the cache's format, RoPE keys turned to
     their positions."""
-    _check(load_library().hra_cache_append(ctypes.byref(p), ctypes.c_void_p(_launch_stream(p, stream))))
+    _launch("hra_cache_append", p, stream)
 
 
 def make_load_params(ckv, krope, seq_lens, out, *, block_table=None, page_size: int = 0, seq_stride: int = 0,
@@ -495,4 +495,4 @@ def make_load_params(ckv, krope, seq_lens, out, *, block_table=None, page_size: 
 def cache_load(p: HraLoadParams, stream=None) -> None:
     """Read cached rows back as contiguous bf16 rows [C_KV | K_RoPE], the form mlra_prefill
     takes."""
-    _check(load_library().hra_cache_load(ctypes.byref(p), ctypes.c_void_p(_launch_stream(p, stream))))
+    _launch("hra_cache_load", p, stream)
