@@ -35,6 +35,9 @@ hra_status done(cudaError_t e, const char* what) {
   return HRA_OK;
 }
 
+// Most tokens of a call: token numbers and a grid's strides past them stay below 2^31.
+constexpr int kMaxTokens = 1 << 30;
+
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 hra_status check_pointer(const void* p, unsigned n, const char* name) {
@@ -97,6 +100,7 @@ hra_status run_plan(const hra_plan_params* p, cudaStream_t stream) {
   if (p->max_pages < 1 || p->num_pages < 1 || p->max_tokens < 1)
     return fail(HRA_ERR_INVALID_ARG, "max_pages=%d, num_pages=%d, max_tokens=%d must be >= 1", p->max_pages, p->num_pages,
                 p->max_tokens);
+  if (p->max_tokens > kMaxTokens) return fail(HRA_ERR_UNSUPPORTED, "max_tokens=%d is above 2^30", p->max_tokens);
   if (static_cast<long long>(p->batch) * p->max_pages > INT_MAX || static_cast<long long>(p->max_pages) * p->page_size > INT_MAX ||
       static_cast<long long>(p->num_pages) * p->page_size > INT_MAX)
     return fail(HRA_ERR_UNSUPPORTED, "batch * max_pages, max_pages * page_size and num_pages * page_size must be below 2^31");
@@ -150,6 +154,7 @@ hra_status read_plan_status(const hra_plan_params* p, cudaStream_t stream) {
 hra_status run_append(const hra_append_params* p, cudaStream_t stream) {
   if (p == nullptr) return fail(HRA_ERR_INVALID_ARG, "params is NULL");
   if (p->n_tokens < 1) return fail(HRA_ERR_INVALID_ARG, "n_tokens=%d must be >= 1", p->n_tokens);
+  if (p->n_tokens > kMaxTokens) return fail(HRA_ERR_UNSUPPORTED, "n_tokens=%d is above 2^30", p->n_tokens);
   const CacheView c = {p->d_c, p->d_rope, p->ckv, p->krope, p->ckv_stride, p->krope_stride, p->cache_rows, p->cache_dtype,
                        p->ckv_scale, p->ckv_scale_stride, p->scale_block};
   hra_status st = check_cache(c);
@@ -199,6 +204,7 @@ hra_status run_load(const hra_load_params* p, cudaStream_t stream) {
   if (p->batch < 1 || p->batch > hra::kMaxBatch)
     return fail(HRA_ERR_UNSUPPORTED, "batch=%d (supported: 1..%d)", p->batch, hra::kMaxBatch);
   if (p->max_tokens < 1) return fail(HRA_ERR_INVALID_ARG, "max_tokens=%d must be >= 1", p->max_tokens);
+  if (p->max_tokens > kMaxTokens) return fail(HRA_ERR_UNSUPPORTED, "max_tokens=%d is above 2^30", p->max_tokens);
   const CacheView c = {p->d_c, p->d_rope, p->ckv, p->krope, p->ckv_stride, p->krope_stride, p->cache_rows, p->cache_dtype,
                        p->ckv_scale, p->ckv_scale_stride, p->scale_block};
   hra_status st = check_cache(c);

@@ -280,7 +280,7 @@ HRA_API hra_status hra_check_prefill_status(const hra_prefill_params* p, void* s
  * replayed with any number of tokens up to max_tokens.
  * seq_lens_out and free_range_out may be seq_lens and free_range themselves; no other buffers may
  * overlap.  With buffers of their own, the same call can be made again and gives the same plan.
- * 1 <= batch <= 1024; page_size a multiple of 32; batch * max_pages, max_pages * page_size and
+ * 1 <= batch <= 1024; 1 <= max_tokens <= 2^30; page_size a multiple of 32; batch * max_pages, max_pages * page_size and
  * num_pages * page_size below 2^31.  Pointers 4-byte aligned (free_range 8); one launch, no workspace.
  */
 typedef struct {
@@ -323,7 +323,7 @@ HRA_API hra_status hra_check_plan_status(const hra_plan_params* p, void* stream)
  * A latent that is no finite number makes its block's scale no finite number.
  * rows_out (optional): what the cache now stands for, bf16 [n_tokens, d_c + 64] (latent rounded to
  * bf16, turned RoPE key), the rows that mlra_prefill reads; rows of skipped tokens are left.
- * d_c in {128, 256, 512}, d_rope = 64; 1 <= n_tokens < 2^31.  latent, krope_in, ckv, krope and
+ * d_c in {128, 256, 512}, d_rope = 64; 1 <= n_tokens <= 2^30.  latent, krope_in, ckv, krope and
  * rows_out 16-byte aligned, bf16 strides multiples of 8, 8-bit ones of 16, all below 2^31.  No two buffers
  * overlap.  One launch, no workspace.
  */
@@ -353,7 +353,7 @@ HRA_API hra_status hra_cache_append(const hra_append_params* p, void* stream /* 
  * mlra_prefill reads: out[b, t] for t < min(seq_lens[b], max_tokens), 8-bit latents as
  * code * scale rounded once to bf16.  Rows behind a sequence's last are left as they were; a row whose
  * page is not in the cache is zero.  The cache is described as in hra_decode_params.
- * d_c in {128, 256, 512}, d_rope = 64; 1 <= batch <= 1024.  out 16-byte aligned, its strides
+ * d_c in {128, 256, 512}, d_rope = 64; 1 <= batch <= 1024; 1 <= max_tokens <= 2^30.  out 16-byte aligned, its strides
  * multiples of 8.  One launch, no workspace.
  */
 typedef struct {

@@ -110,7 +110,7 @@ def _plan(**over):
     (dict(batch=0), B.HRA_ERR_UNSUPPORTED), (dict(batch=1025), B.HRA_ERR_UNSUPPORTED),
     (dict(page_size=0), B.HRA_ERR_UNSUPPORTED), (dict(page_size=48), B.HRA_ERR_UNSUPPORTED),
     (dict(max_pages=0), B.HRA_ERR_INVALID_ARG), (dict(num_pages=0), B.HRA_ERR_INVALID_ARG),
-    (dict(max_tokens=0), B.HRA_ERR_INVALID_ARG),
+    (dict(max_tokens=0), B.HRA_ERR_INVALID_ARG), (dict(max_tokens=2**30 + 1), B.HRA_ERR_UNSUPPORTED),
     (dict(max_pages=1 << 26), B.HRA_ERR_UNSUPPORTED), (dict(num_pages=1 << 26), B.HRA_ERR_UNSUPPORTED),
     (dict(batch=1024, max_pages=1 << 21), B.HRA_ERR_UNSUPPORTED),
     (dict(seq_lens=0), B.HRA_ERR_INVALID_ARG), (dict(slots=0), B.HRA_ERR_INVALID_ARG),
@@ -152,7 +152,7 @@ CACHE_REFUSALS = [
 
 
 @pytest.mark.parametrize("over,status", CACHE_REFUSALS + [
-    (dict(n_tokens=0), B.HRA_ERR_INVALID_ARG),
+    (dict(n_tokens=0), B.HRA_ERR_INVALID_ARG), (dict(n_tokens=2**31 - 1), B.HRA_ERR_UNSUPPORTED),
     (dict(latent=0), B.HRA_ERR_INVALID_ARG), (dict(krope_in=0x20008), B.HRA_ERR_INVALID_ARG),
     (dict(slots=0), B.HRA_ERR_INVALID_ARG), (dict(positions=0), B.HRA_ERR_INVALID_ARG),
     (dict(latent_stride=508), B.HRA_ERR_INVALID_ARG), (dict(krope_in_stride=60), B.HRA_ERR_INVALID_ARG),
@@ -179,7 +179,8 @@ def _load(**over):
 
 @pytest.mark.parametrize("over,status", CACHE_REFUSALS + [
     (dict(batch=0), B.HRA_ERR_UNSUPPORTED), (dict(batch=1025), B.HRA_ERR_UNSUPPORTED),
-    (dict(max_tokens=0), B.HRA_ERR_INVALID_ARG), (dict(seq_lens=0), B.HRA_ERR_INVALID_ARG),
+    (dict(max_tokens=0), B.HRA_ERR_INVALID_ARG), (dict(max_tokens=2**31 - 1), B.HRA_ERR_UNSUPPORTED),
+    (dict(seq_lens=0), B.HRA_ERR_INVALID_ARG),
     (dict(out=0), B.HRA_ERR_INVALID_ARG), (dict(out=0x90008), B.HRA_ERR_INVALID_ARG),
     (dict(page_size=40), B.HRA_ERR_UNSUPPORTED), (dict(max_pages=0), B.HRA_ERR_INVALID_ARG),
     (dict(block_table=0, seq_stride=-1), B.HRA_ERR_INVALID_ARG),
