@@ -7,6 +7,8 @@
 // of the decode path therefore reads the outputs of earlier kernels, and writes anything
 // an earlier kernel reads, only after grid_dep_wait.  Each kernel also signals
 // griddepcontrol.launch_dependents early so that the next one can be scheduled.
+// The kernels that write a call's inputs (paged_cache.cu) wait like the others but do not signal
+// early, so that what they write is complete when any kernel of a later call runs.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -29,6 +29,20 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 
+// The end of a block's work.  The decode and prefill kernels load a call's inputs (lengths, block
+// table, cache rows and scales: what is written here) before they wait for the kernels in front of
+// them, some of them behind another kernel of their call that waits in their place.  So these
+// kernels let no dependent start early (no grid_dep_launch): the next kernel is scheduled when every block
+// here has ended, and a block's writes are in memory, for TMA loads too, before it ends (the
+// barrier hands them to one thread's fences).
+__device__ __forceinline__ void publish() {
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    __threadfence();
+    asm volatile("fence.proxy.async.global;" ::: "memory");
+  }
+}
+
 // An element's place, past 32 bits in a long cache.
 __device__ __forceinline__ long long wide(int row, int stride) { return static_cast<long long>(row) * stride; }
 
@@ -59,7 +73,6 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
   __shared__ int ring_s[2];     // the ring's head and tail as places
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = a.batch, P = a.page_size;
   const int n_warps = blockDim.x >> 5;
-  grid_dep_launch();
   grid_dep_wait();
   if (t == 0) bad_s = INT_MAX;
   __syncthreads();
@@ -185,6 +198,7 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
     a.slots[i] = slot;
     if (a.positions != nullptr) a.positions[i] = pos;
   }
+  publish();
 }
 
 // ------------------------------------------------------------------------------- append
@@ -264,7 +278,6 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const A
   const int g = blockIdx.y, groups = a.d_c / 128;
   const int i0 = blockIdx.x * W, n_win = min(W, a.n_tokens - i0);
   const int rows = static_cast<int>(a.cache_rows);
-  grid_dep_launch();
   grid_dep_wait();
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.rows_out);
 
@@ -308,6 +321,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const A
         *reinterpret_cast<uint32_t*>(o + 32) = y2;
       }
     }
+    publish();
     return;
   }
 
@@ -469,6 +483,7 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const A
       __syncthreads();  // warp_max is written again
     }
   }
+  publish();
 }
 
 // --------------------------------------------------------------------------------- load
@@ -481,7 +496,6 @@ constexpr int kLoadTokens = 32;  // most of a block
 template <CacheFormat F>
 __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs a, int per_block) {
   __shared__ int row_s[kLoadTokens];
-  grid_dep_launch();
   grid_dep_wait();
   const int b = blockIdx.y, t0 = blockIdx.x * per_block;
   const int n = min(min(a.seq_lens[b], a.max_tokens) - t0, per_block);
@@ -525,6 +539,7 @@ __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs
     if (row >= 0) v = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.krope) + wide(row, a.krope_stride) + c);
     *reinterpret_cast<uint4*>(out + wide(r, a.out_stride) + a.d_c + c) = v;
   }
+  publish();
 }
 
 }  // namespace

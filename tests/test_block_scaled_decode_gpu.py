@@ -418,3 +418,105 @@ def test_two_decodes_at_once():
     for p, bufs, _, ref, stream in kept:
         hra.check_device_status(p, stream)
         assert_parity(bufs[4].cpu().numpy(), ref, "two streams")
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("fmt", ["bf16", "int8", "e4m3"])
+def test_steps_queued_back_to_back(fmt, graph):
+    """Plan, append and decode of two steps in turn on the same buffers, with nothing between the
+    calls: each decode sees its own step's lengths, pages and rows, bit for bit what it sees when every call
+    is waited for (no sum's order depends on timing).  Few heads and long appends leave SMs to kernels
+    that start early."""
+    r = np.random.default_rng(5)
+    page, wide, h, most = 64, 200, 16, 12000
+    fmt_t = {**DTYPE, "bf16": torch.bfloat16}[fmt]
+    i32 = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")  # noqa: E731
+    block = 0 if fmt == "bf16" else 64
+    pages = 2 * wide
+    codes = torch.zeros(pages * page, 512, dtype=fmt_t, device="cuda")
+    scale = torch.zeros(pages * page // 64, 4, device="cuda") if block else None
+    krope = torch.zeros(pages * page, 64, dtype=torch.bfloat16, device="cuda")
+    lens, table, lens_out, start, status = i32(2), i32(2, wide), i32(2), i32(3), i32(4)
+    slots, positions = i32(most), i32(most)
+    ring = torch.arange(pages, dtype=torch.int32, device="cuda")
+    free, free_out = (torch.tensor([0, pages], dtype=torch.int64, device="cuda") for _ in range(2))
+    q = torch.tensor(r.standard_normal((2, h, 192)), dtype=torch.bfloat16, device="cuda")
+    w_uk, w_uv = (torch.tensor(r.standard_normal((h, 512, 128)) / 128 ** 0.5, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    steps = []
+    for asks in ((5000, 7000), (9, 11900), (7000, 1)):
+        rows = torch.tensor(r.standard_normal((most, 576)), dtype=torch.bfloat16, device="cuda")
+        new = torch.tensor(asks, dtype=torch.int32, device="cuda")
+        steps.append((
+            hra.make_plan_params(lens, new, table, ring, free, lens_out, free_out, start, slots, status, positions=positions, page_size=page),
+            hra.make_append_params(rows[:, :512], rows[:, 512:], slots, positions, codes, krope, ckv_scale=scale, scale_block=block),
+            [torch.zeros(2, h, 128, device="cuda") for _ in range(5)], (rows, new)))
+    ws = None
+
+    def queue(k, turn, wait):
+        nonlocal ws
+        plan, put, outs, _ = steps[k]
+        dec = hra.make_params(q, codes, krope, lens_out, w_uk, w_uv, outs[turn], n_branch=4, branch_scale=0.5, block_table=table,
+                              page_size=page, ckv_scale=scale, scale_block=block)
+        if ws is None:
+            ws = hra.alloc_workspace(dec)
+        else:
+            dec.workspace, dec.workspace_bytes = ws.data_ptr(), ws.numel()
+        for call, p in ((hra.page_plan, plan), (hra.cache_append, put), (hra.mlra_decode, dec)):
+            call(p)
+            if wait:
+                torch.cuda.synchronize()
+        return dec
+
+    for k in range(3):
+        hra.check_device_status(queue(k, 0, True))
+        hra.check_plan_status(steps[k][0])
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for turn in range(1, 5):
+                for k in range(3):
+                    queue(k, turn, False)
+        g.replay()
+    else:
+        for turn in range(1, 5):
+            for k in range(3):
+                queue(k, turn, False)
+    torch.cuda.synchronize()
+    for k, (_, _, outs, _) in enumerate(steps):
+        assert outs[0].abs().max() > 0 and torch.isfinite(outs[0]).all()
+        for turn in range(1, 5):
+            assert torch.equal(outs[turn], outs[0]), (k, turn)
+
+
+def test_load_then_prefill_queued_back_to_back():
+    """Two caches loaded in turn into one buffer, each followed at once by the prefill that reads it."""
+    r = np.random.default_rng(6)
+    L, n, h = 4000, 64, 16
+    w_uk, w_uv = (torch.tensor(r.standard_normal((h, 512, 128)) / 128 ** 0.5, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q = torch.tensor(r.standard_normal((n, h, 192)), dtype=torch.bfloat16, device="cuda")
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    loaded = torch.zeros(1, L, 576, dtype=torch.bfloat16, device="cuda")
+    loads, ws, outs = [], None, [[torch.zeros(n, h, 128, device="cuda") for _ in range(5)] for _ in range(2)]
+    for _ in range(2):
+        codes = torch.tensor(r.integers(-127, 128, (L, 512)), dtype=torch.int8, device="cuda")
+        scale = torch.tensor(r.random((-(-L // 64), 4)) / 64 + 1e-3, dtype=torch.float32, device="cuda")
+        krope = torch.tensor(r.standard_normal((L, 64)), dtype=torch.bfloat16, device="cuda")
+        loads.append((hra.make_load_params(codes, krope, lens, loaded, seq_stride=L, ckv_scale=scale, scale_block=64), codes, scale, krope))
+    for turn in range(5):
+        for k in range(2):
+            pre = hra.make_prefill_params(q, loaded[0, :, :512], loaded[0, :, 512:], w_uk, w_uv, outs[k][turn], n_branch=4, branch_scale=0.5)
+            if ws is None:
+                ws = hra.alloc_prefill_workspace(pre)
+            else:
+                pre.workspace, pre.workspace_bytes = ws.data_ptr(), ws.numel()
+            hra.cache_load(loads[k][0])
+            if turn == 0:
+                torch.cuda.synchronize()
+            hra.mlra_prefill(pre)
+            if turn == 0:
+                hra.check_prefill_status(pre)
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert outs[k][0].abs().max() > 0
+        for turn in range(1, 5):
+            assert torch.equal(outs[k][turn], outs[k][0]), (k, turn)
