@@ -83,7 +83,7 @@ absorb_tc_kernel(const __grid_constant__ CUtensorMap map_wuk, const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    grid_dep_launch();
+    if (!a.late_release) grid_dep_launch();
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
     *abort_flag = 0;
@@ -129,6 +129,7 @@ absorb_tc_kernel(const __grid_constant__ CUtensorMap map_wuk, const __grid_const
   // Everything above reads only inputs of the call; what follows writes the workspace,
   // which the previous call's kernels read, so it waits for them.
   grid_dep_wait();
+  if (a.late_release && threadIdx.x == 0) grid_dep_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 3)
     tile_prefix_warp(a.seq_lens, a.batch, a.tile_tokens, a.tile_prefix);
   const int r = 32 * (warp & 3) + lane;  // sequence within the chunk = TMEM lane

@@ -20,6 +20,10 @@ struct AbsorbArgs {
   int d_c;                    // latent width: 512, or 256 / 128 (a shard of 128-wide branches)
   float alpha_q, alpha_kv, rope_theta;
   const int32_t* q_positions; // [B] query position per sequence, or nullptr: seq_lens[s] - 1
+  // 1: the decode kernel, which loads lengths, block table, scales and cache ahead of its own wait, is
+  // started only once everything in front of this call is complete and visible (free with block
+  // scales; without them 1 us at h = 16, so 0 there)
+  int late_release;
 };
 
 constexpr int kMaxOutPeers = 7;  // other ranks' out buffers the up-projection can add into

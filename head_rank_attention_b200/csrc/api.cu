@@ -278,6 +278,7 @@ hra_status run_decode(const hra_decode_params* p, cudaStream_t stream) {
   ab.tile_prefix = tile_prefix;
   ab.tile_tokens = hra::decode_tile_tokens(dc / p->n_branch, p->scale_block);
   ab.q_positions = p->q_positions;
+  ab.late_release = p->scale_block > 1 ? 1 : 0;
   // Programmatic dependent launch lets each kernel start while the previous one drains;
   // the stage-timing mode launches plainly so that its events bracket whole kernels.
   const bool pdl = p->stage_events == nullptr;

@@ -7,8 +7,9 @@
 // of the decode path therefore reads the outputs of earlier kernels, and writes anything
 // an earlier kernel reads, only after grid_dep_wait.  Each kernel also signals
 // griddepcontrol.launch_dependents early so that the next one can be scheduled.
-// The kernels that write a call's inputs (paged_cache.cu) wait like the others but do not signal
-// early, so that what they write is complete when any kernel of a later call runs.
+// The kernels that write later calls' inputs (paged_cache.cu) do not signal, and the first kernel of a
+// block-scaled decode and of a prefill does so only after its own wait: all that was in
+// front of the call is then complete for the call's other kernels.
 #pragma once
 
 #include <cuda_runtime.h>

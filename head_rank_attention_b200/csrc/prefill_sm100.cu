@@ -49,9 +49,11 @@ __global__ void prefill_prep_kernel(const PrefillArgs a) {
   __shared__ double turns[32];  // rotation pair d turns by theta^(-2d/64) / (2 pi) per position
   if (threadIdx.x < 32) turns[threadIdx.x] = pow(static_cast<double>(a.rope_theta), -2.0 * threadIdx.x / 64.0) *
                                              0.15915494309189535;
-  if (threadIdx.x == 0) grid_dep_launch();
   __syncthreads();
   grid_dep_wait();  // q16 / kr16 are read by the previous call's attention
+  // Not before the wait: the expansion loads the latent ahead of its own wait, and a kernel in
+  // front of this call may be writing it.
+  if (threadIdx.x == 0) grid_dep_launch();
   const int nq = a.n_query * a.heads;
   const long long total = static_cast<long long>(nq) + a.l_pad;
   for (long long r = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; r < total;
