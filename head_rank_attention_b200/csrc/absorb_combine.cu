@@ -64,6 +64,7 @@ __device__ __forceinline__ void store_q32(const AbsorbArgs& a, long long dst, co
 // grid (h, ceil(B / 128), max(d_c / 256, 1) latent parts), 256 threads, two CTAs per SM.
 // Warp w owns the sequences of TMEM lane quadrant w % 4 and 128 of the CTA's
 // min(d_c, 256) latent columns (w / 4; with 128 columns warps 4-7 only rotate q_rope).
+template <bool LATE>  // see launch_absorb_q's late_release
 __global__ void __launch_bounds__(AbsorbCfg::THREADS, 1)
 absorb_tc_kernel(const __grid_constant__ CUtensorMap map_wuk, const __grid_constant__ CUtensorMap map_q,
                  const AbsorbArgs a) {
@@ -83,7 +84,7 @@ absorb_tc_kernel(const __grid_constant__ CUtensorMap map_wuk, const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    if (!a.late_release) grid_dep_launch();
+    if (!LATE) grid_dep_launch();
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
     *abort_flag = 0;
@@ -129,7 +130,7 @@ absorb_tc_kernel(const __grid_constant__ CUtensorMap map_wuk, const __grid_const
   // Everything above reads only inputs of the call; what follows writes the workspace,
   // which the previous call's kernels read, so it waits for them.
   grid_dep_wait();
-  if (a.late_release && threadIdx.x == 0) grid_dep_launch();
+  if (LATE && threadIdx.x == 0) grid_dep_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 3)
     tile_prefix_warp(a.seq_lens, a.batch, a.tile_tokens, a.tile_prefix);
   const int r = 32 * (warp & 3) + lane;  // sequence within the chunk = TMEM lane
@@ -761,10 +762,11 @@ int absorb_seq_chunk(int) { return 128; }
 int upproj_seq_chunk() { return 32; }
 
 cudaError_t launch_absorb_q(const CUtensorMap& map_wuk, const CUtensorMap& map_q, const AbsorbArgs& a,
-                            cudaStream_t stream, bool pdl) {
-  cudaError_t e = set_smem(absorb_tc_kernel, AbsorbCfg::SMEM);
+                            cudaStream_t stream, bool pdl, bool late_release) {
+  auto kern = late_release ? absorb_tc_kernel<true> : absorb_tc_kernel<false>;
+  cudaError_t e = set_smem(kern, AbsorbCfg::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_kernel(absorb_tc_kernel, dim3(a.heads, (a.batch + 127) / 128, a.d_c > 256 ? a.d_c / 256 : 1),
+  return launch_kernel(kern, dim3(a.heads, (a.batch + 127) / 128, a.d_c > 256 ? a.d_c / 256 : 1),
                        dim3(AbsorbCfg::THREADS),
                        AbsorbCfg::SMEM, stream, pdl, map_wuk, map_q, a);
 }

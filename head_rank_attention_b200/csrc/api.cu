@@ -278,11 +278,10 @@ hra_status run_decode(const hra_decode_params* p, cudaStream_t stream) {
   ab.tile_prefix = tile_prefix;
   ab.tile_tokens = hra::decode_tile_tokens(dc / p->n_branch, p->scale_block);
   ab.q_positions = p->q_positions;
-  ab.late_release = p->scale_block > 1 ? 1 : 0;
   // Programmatic dependent launch lets each kernel start while the previous one drains;
   // the stage-timing mode launches plainly so that its events bracket whole kernels.
   const bool pdl = p->stage_events == nullptr;
-  e = hra::launch_absorb_q(map_wuk, map_q, ab, stream, pdl);
+  e = hra::launch_absorb_q(map_wuk, map_q, ab, stream, pdl, p->scale_block > 1);
   if (e != cudaSuccess) return cuda_fail(e, "absorb_q launch");
 
   const float tau = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(192.0f);

@@ -6,13 +6,13 @@
 //   the step.  One request per thread; exclusive prefix sums of the tokens, of the pages
 //   taken and of the pages given back place everything.  A few kilobytes are read and
 //   written: latency bounds it, so it is one launch, each block scanning all lengths itself
-//   (3.1 us for 64 requests, 6.8 us for 1024 with 65536 tokens).
+//   (3.3 us for 64 requests, 6.4 us for 1024 with 65536 tokens).
 // append: a cache row is the token's latent in the cache's format and its RoPE key turned
 //   by the token's position.  With one scale per block of tokens and 128-wide latent head,
 //   s = max|x| / top over the block; a block that grows token by token keeps the larger of
 //   its old scale and the new tokens', and the rows it already holds are brought to it.
 //   2 (d_c + 64) bytes a token in, d_c + 128 of cache and 2 (d_c + 64) of rows out: 5.5 us for 6.8 k
-//   tokens of 512 columns (3.0 us of HBM time), 3.0 us for a step of 64 tokens.
+//   tokens of 512 columns (3.0 us of HBM time), 2.8 us for a step of 64 tokens.
 // load: rows c * s and RoPE keys back as bf16, the form prefill reads.  HBM bounds it: 53 us for
 //   160 k rows of 512 columns, 87 % of the rate of a plain copy.
 #include <climits>
@@ -33,7 +33,7 @@ constexpr uint32_t kAll = 0xffffffffu;
 // they wait for the kernels in front of them, behind a first kernel that waits in their place.  So no
 // kernel here signals early (no grid_dep_launch): the next one starts when every block has ended.
 // Where the call's first kernel starts the others only after its own wait (block-scaled decode:
-// AbsorbArgs::late_release; prefill) that is enough.  A decode of the other formats does not, so the
+// launch_absorb_q's late_release; prefill) that is enough.  A decode of the other formats does not, so the
 // page plan and the append to them end each block with publish: its writes are in memory, for
 // TMA loads too (the barrier hands them to one thread's fences).  0.4 us; on every kernel it
 // would be 1.8 us for 24 k tokens of a branch and 4 for 160 k loaded rows.
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream) {
   // A thread for a sequence, and a token or so for a thread: a step of 64 requests is one block of
-  // 128, and 65536 tokens are spread over 64 SMs (11.8 us on one cluster's 8, 6.8 so).
+  // 128, and 65536 tokens are spread over 64 SMs (11.8 us on one cluster's 8, 6.4 so).
   // Blocks that read lengths which another block overwrites must meet, in one cluster.
   const int threads = (a.batch > kPlanMinThreads ? a.batch + 31 : kPlanMinThreads) / 32 * 32;
   const int blocks = (a.max_tokens + threads - 1) / threads;
@@ -571,7 +571,7 @@ cudaError_t launch_cache_append(CacheFormat format, const AppendArgs& a, cudaStr
 }
 
 cudaError_t launch_cache_load(CacheFormat format, const LoadArgs& a, cudaStream_t stream) {
-  // Blocks of 32 tokens, or of 16 where that leaves SMs idle (2048 tokens: 2.95 instead of 3.46 us;
+  // Blocks of 32 tokens, or of 16 where that leaves SMs idle (2048 tokens: 0.5 us less, 2.5 in all;
   // long loads gain 2 % from the larger).
   const int per_block = static_cast<long long>((a.max_tokens + kLoadTokens - 1) / kLoadTokens) * a.batch < 2 * 148 ? 16 : kLoadTokens;
   const dim3 grid((a.max_tokens + per_block - 1) / per_block, a.batch);
