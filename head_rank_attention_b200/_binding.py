@@ -185,19 +185,22 @@ def _on_one_device(p, tensors) -> None:
     if len(devices) != 1:
         raise ValueError(f"the tensors lie on several devices: {sorted(map(str, devices))}")
     p._device = devices.pop()
+    p._index = p._device.index if p._device.type == "cuda" else None
 
 
 def _launch(name: str, p, stream) -> None:
     """Call an entry point with p on a stream (the current one by default).  p's tensors must be
     on the current device, which is the one that the kernel runs on."""
     import torch
-    device = p._device
-    current = torch.cuda.current_device() if device.type == "cuda" else None
-    if device.index != current or current is None:
-        raise ValueError(f"the tensors are on {device}, "
-                         + ("not on a CUDA device" if current is None else f"the current device is cuda:{current}"))
+    if p._index is None:
+        raise ValueError(f"the tensors are on {p._device}, not on a CUDA device")
+    current = torch._C._cuda_getDevice()  # torch.cuda.current_device() without its check that CUDA is up
+    if current != p._index:
+        raise ValueError(f"the tensors are on {p._device}, the current device is cuda:{current}")
     handle = torch._C._cuda_getCurrentRawStream(current) if stream is None else getattr(stream, "cuda_stream", stream)
-    _check(getattr(load_library(), name)(ctypes.byref(p), handle))
+    status = getattr(_lib or load_library(), name)(ctypes.byref(p), handle)
+    if status != HRA_OK:
+        _check(status)
 
 
 def _ptr(t) -> int:
