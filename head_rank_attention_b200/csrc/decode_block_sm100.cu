@@ -68,7 +68,7 @@ struct BlockCfg {
   // Two rings.  A tile's copy (codes, and the RoPE key, converted in place) is held until its
   // QK has run; its fp16 latent (columns 0-63, 64-127) from the conversion until its P.V has.
   // One ring for both (36 KB a tile, held 7900 cycles from copy to P.V) made 1980 cycles a tile.
-    static constexpr int RAW = 4, LAT = 4;
+  static constexpr int RAW = 4, LAT = 4;
   static constexpr int RAW_BYTES = 2 * BOX_BYTES, LAT_BYTES = 2 * BOX_BYTES;
   static constexpr int PAR = 8;  // chunk parameters outlive the copy: until the tile's softmax
   static constexpr int CHUNKS = NT / 32;
@@ -221,7 +221,7 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* never_flag = abort_flag + 1;  // stays 0: exit-path waits ignore the abort flag
   float2* ml = reinterpret_cast<float2*>(misc + C::BAR_BYTES);  // [2 streams][128]
-  ChunkParams* params = reinterpret_cast<ChunkParams*>(misc + C::BAR_BYTES + C::ML_BYTES);  // [STAGES][CHUNKS]
+  ChunkParams* params = reinterpret_cast<ChunkParams*>(misc + C::BAR_BYTES + C::ML_BYTES);  // [PAR][CHUNKS]
   int* prefix = reinterpret_cast<int*>(misc + C::BAR_BYTES + C::ML_BYTES + C::PAR_BYTES);
 
   const int warp = threadIdx.x >> 5;
