@@ -215,6 +215,18 @@ __device__ __forceinline__ bool group_live(int g, int G, int T) {
   return t0 != t1;
 }
 
+// A partial state (M, l) as the merges read it.  M is a maximum, which passes over scores that are
+// no numbers, while l, a sum, is none once one of them is: a segment with nothing else has (-inf,
+// NaN).  M = -inf stands for "no tokens" from here on, so such a state gets a finite M, under which
+// its l reaches the denominator whatever the weight.
+__device__ __forceinline__ float2 partial_state(float2 ml) {
+  if (ml.y != ml.y) ml.x = 0.f;
+  return ml;
+}
+
+// 1 / den, or 0 where there were no tokens (den = 0); a den that is no number stays one.
+__device__ __forceinline__ float inverse_or_zero(float den) { return den == 0.f ? 0.f : 1.f / den; }
+
 // ---------------------------------------------------------------------------- merge
 // grid (ceil(h / (256 / TPH)), d_c / 128 slices, B), 256 * Z threads.  Thread = (head, CPT
 // consecutive latent columns of the slice); the Z thread sets take alternate runs of GU
@@ -249,7 +261,7 @@ __global__ void __launch_bounds__(256 * Z) merge_kernel(const CombineArgs a) {
         // a group with an empty tile range (more groups than tiles) wrote nothing
         const bool live = g <= g_hi && group_live(g, G, T);
         const long long row = ((static_cast<long long>(g) + seq) * gridDim.y + slice) * 128 + head;
-        ml[u] = live ? a.ml_part[row] : make_float2(-INFINITY, 0.f);
+        ml[u] = live ? partial_state(a.ml_part[row]) : make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int v = 0; v < V; ++v)
           o[u][v] = live ? *reinterpret_cast<const float4*>(a.o_part + row * 128 + col + 4 * v)
@@ -299,7 +311,7 @@ __global__ void __launch_bounds__(256 * Z) merge_kernel(const CombineArgs a) {
     M = mx;  // den and acc are now relative to the larger maximum
   }
   if (head >= a.heads) return;
-  const float inv = den > 0.f ? 1.f / den : 0.f;  // an empty sequence gives zeros
+  const float inv = inverse_or_zero(den);  // an empty sequence gives zeros
   if constexpr (PARTIAL) {
     // the state of this token range: the normalised latent row and log2 of its softmax
     // denominator (sum_t 2^(score_t log2 e) = 2^M * den)
@@ -308,7 +320,7 @@ __global__ void __launch_bounds__(256 * Z) merge_kernel(const CombineArgs a) {
 #pragma unroll
     for (int v = 0; v < CPT / 4; ++v)
       dst[v] = make_float4(acc[4 * v] * inv, acc[4 * v + 1] * inv, acc[4 * v + 2] * inv, acc[4 * v + 3] * inv);
-    if (col == 0) a.part_lse[hs * gridDim.y + slice] = den > 0.f ? M + log2f(den) : -INFINITY;
+    if (col == 0) a.part_lse[hs * gridDim.y + slice] = den == 0.f ? -INFINITY : M + log2f(den);
     return;
   }
   // o_lat as hi / lo bf16 terms, [h][B][d_c] each
@@ -610,7 +622,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) combine_small_kernel(const C
       const bool live = q < pre[SB] && group_live(g, G, T);
       const int row = ((g + s) * slices + c) * 128 + i;  // < (65535 + 1024) * 4 * 128
       sq[u] = s;
-      ml[u] = live ? a.ml_part[row] : make_float2(-INFINITY, 0.f);
+      ml[u] = live ? partial_state(a.ml_part[row]) : make_float2(-INFINITY, 0.f);
       o[u] = live ? a.o_part[static_cast<long long>(row) * 128 + j] : 0.f;
     }
 #pragma unroll
@@ -648,7 +660,7 @@ __global__ void __launch_bounds__(kSmallThreads, 2) combine_small_kernel(const C
         num = fmaf(wt, x_acc[k][s][j], num);
       }
     }
-    o_lat[s][j] = d > 0.f ? num / d : 0.f;  // an empty sequence gives zeros
+    o_lat[s][j] = d == 0.f ? 0.f : num / d;  // an empty sequence gives zeros
   }
   __syncthreads();
 
@@ -712,7 +724,10 @@ __global__ void __launch_bounds__(256) partial_combine_kernel(const CombineArgs 
   const long long part_o = static_cast<long long>(a.batch) * a.heads * a.d_c;     // elements per part
   const long long part_l = static_cast<long long>(a.batch) * a.heads * slices;
   float m = -INFINITY;
-  for (int r = 0; r < a.n_parts; ++r) m = fmaxf(m, a.parts_lse[r * part_l + hs * slices + slice]);
+  for (int r = 0; r < a.n_parts; ++r) {
+    const float lse = a.parts_lse[r * part_l + hs * slices + slice];
+    m = fmaxf(m, lse != lse ? 0.f : lse);  // not -inf: a range whose state is no number is not empty
+  }
   float acc[CPT];
 #pragma unroll
   for (int u = 0; u < CPT; ++u) acc[u] = 0.f;
@@ -734,7 +749,7 @@ __global__ void __launch_bounds__(256) partial_combine_kernel(const CombineArgs 
       }
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;  // every range empty: zeros
+  const float inv = inverse_or_zero(wsum);  // every range empty: zeros
   const long long base = (static_cast<long long>(head) * a.batch + seq) * a.d_c + 128 * slice + col;
   __align__(16) __nv_bfloat16 hi[CPT], lo[CPT];
 #pragma unroll

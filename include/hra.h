@@ -159,8 +159,9 @@ typedef struct {
      and part_lse set the call stops after the split-KV merge and writes, for every
      (sequence, head, 128-column slice of the latent), the slice's softmax-weighted latent
      row over its tokens (normalised) and the log2 of the slice's softmax denominator
-     (log2 sum_t exp(score_t); -inf for an empty range, with a zero row).  out is then
-     neither read nor written (it may be NULL).  The devices gather these states and one
+     (log2 sum_t exp(score_t); -inf for an empty range, with a zero row; no number, in
+     both, for a range that read a scale which is none).  out is then neither read nor
+     written (it may be NULL).  The devices gather these states and one
      hra_combine_partials call merges them and finishes the decode.                      */
   const int32_t* q_positions;   /* [B] position of each sequence's query, or NULL: L - 1   */
   float* part_o;                /* fp32 [B, h, d_c], 16-B aligned, or NULL                 */
