@@ -7,14 +7,17 @@
 // accumulation.  What a block scale changes is the arithmetic around them.
 //
 // Scales.  All rows of a 32-row chunk share the scale s = f * 2^e (f in [1, 2)).  The
-// converter writes code * 2^(e - E), which is exact in fp16, with E the largest exponent of the
-// tile's chunks, kept in [kMinExp, kMaxExp]; the RoPE key is divided by sigma = f * 2^E in
-// fp32 and rounded once.  The MMA then gives score / sigma for the latent and the RoPE part
-// alike, and the softmax multiplies by its chunk's sigma: no rounding of a scale enters the
-// scores.  The values need f * 2^E as well: the softmax works on x = score + log2(sigma), so that
-// P = 2^(x - M) times the converted tile is the scaled value, and the denominator adds
-// P / sigma, one multiplication per chunk.  M is then the largest weight times scale, and
-// partial states keep their meaning: (M, l) with O and l both in units of 2^M.
+// converter writes code * 2^(e - E), with E = e kept in [kMinExp, kMaxExp]: the codes themselves,
+// but for scales outside that range, whose codes are shifted (a value is resolved to
+// 2^(kMinExp - 24)).  The RoPE key is divided by sigma = f * 2^E in fp32 and rounded to fp16 (half a
+// step is 2^-11 of it, or 2^-21 sigma where that is more).  The MMA then gives score / sigma for
+// the latent and the RoPE part alike, and the softmax multiplies by its chunk's sigma: the scale
+// enters the latent's scores without a rounding.  The values need f * 2^E as well: the softmax works
+// on x = score + log2(sigma), so that P = 2^(x - M) times the converted tile is the scaled value,
+// and the denominator adds P / sigma, one multiplication per chunk.  M is then the largest weight
+// times scale, P (fp16) is rounded by 2^-11 of itself or 2^-25 of that largest, and partial states
+// keep their meaning: (M, l) with O and l both in units of 2^M.  E is the chunk's own: with one for
+// the tile, codes beside a scale 2^25 times theirs vanished, and RoPE keys became subnormal.
 //
 // Work decomposition: schedule.cuh, with 96-token tiles.  Even and odd tiles of a CTA are two
 // streams, each with its own softmax warpgroup, score buffer, O and (M, l): one stream's
@@ -315,17 +318,14 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
       int issued = ahead;
       bool ok = true;
       for (int it0 = 0; ok && it0 < ntiles; it0 += TPB) {
-        // this lane's chunk: s = f * 2^e; E is the tile's largest e
+        // this lane's chunk: s = f * 2^e
         const uint32_t bits = __float_as_uint(scale);
         const int ex = static_cast<int>(bits >> 23) - 127;  // s >= 0
         const bool none = bits < 0x00800000u;                 // zero (or subnormal: taken as zero)
         const bool bad = bits >= 0x7F800000u;                 // Inf, NaN (or negative)
         const int e = none || bad ? -127 : ex;
         const float f = bad ? __uint_as_float(0x7FC00000u) : none ? 1.f : __uint_as_float((bits & 0x007FFFFFu) | 0x3F800000u);
-        int E = e;
-#pragma unroll
-        for (int r = 0; r < CHUNKS; ++r) E = max(E, __shfl_sync(kAll, e, min(my_tile * CHUNKS + r, 31)));
-        E = min(max(E, kMinExp), kMaxExp);
+        const int E = min(max(e, kMinExp), kMaxExp);
         const float sigma = f * __uint_as_float(static_cast<uint32_t>(E + 127) << 23);
         ChunkParams cp;
         cp.k = sigma * a.scale_log2;

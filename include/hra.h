@@ -173,7 +173,9 @@ typedef struct {
      then holds d_c + 2 * d_rope bytes per token.  A scale is finite and >= 0 (a scale that is no
      number makes the output of the sequences that read it no number); the values it
      stands for, |code * scale|, stay below 65504; |krope| and the query's |q_rope| stay below
-     4000.  Scales differ freely from block to block; a value is resolved to 2^-32.  ckv_scale has
+     4000.  Scales differ freely from block to block: a value is resolved to 2^-32 (a scale below 2^-32
+     counts as 0), and, with S for a scale but at least 2^-8, a RoPE key to 2^-11 of itself or 2^-20 S,
+     and a softmax weight times S to 2^-11 of itself or 2^-25 of the sequence's largest.  ckv_scale has
      one row for each begun block of cache_rows.  hra_cache_append writes this format.            */
   int scale_block;
 } hra_decode_params;
