@@ -207,7 +207,9 @@ def _ptr(t) -> int:
     return 0 if t is None else int(t.data_ptr())
 
 
-def _cache_format(p, ckv, ckv_scale, scale_block: int) -> None:
+def _cache_format(p, ckv, ckv_scale, scale_block: int, rows: int) -> None:
+    """The format of a cache of `rows` rows; kernels read (the append writes) a scale for each
+    begun block of them and 128 columns."""
     import torch
     p.cache_dtype = {torch.int8: HRA_INT8, torch.float8_e4m3fn: HRA_E4M3}.get(ckv.dtype, HRA_BF16)
     p.scale_block = int(scale_block)
@@ -215,11 +217,16 @@ def _cache_format(p, ckv, ckv_scale, scale_block: int) -> None:
         return
     if ckv_scale is None:
         raise ValueError("an int8 cache needs ckv_scale" if p.cache_dtype == HRA_INT8 else "an e4m3 cache needs ckv_scale")
-    if scale_block > 1:
-        need = (-(-int(ckv.shape[0]) // int(scale_block)), int(ckv.shape[1]) // 128)
-        if (ckv_scale.dtype != torch.float32 or ckv_scale.dim() != 2 or int(ckv_scale.shape[0]) < need[0]
-                or int(ckv_scale.shape[1]) < need[1] or (need[1] > 1 and ckv_scale.stride(1) != 1)):
-            raise ValueError(f"ckv_scale must be float32 {list(need)}, one scale per block of {scale_block} rows and 128 columns")
+    block = max(1, int(scale_block))
+    need = (-(-rows // block), int(ckv.shape[1]) // 128)
+    fits = ckv_scale.dtype == torch.float32 and ckv_scale.dim() in (1, 2) and int(ckv_scale.shape[0]) >= need[0]
+    if fits and ckv_scale.dim() == 2:
+        fits = int(ckv_scale.shape[1]) >= need[1] and (need[1] == 1 or ckv_scale.stride(1) == 1)
+    elif fits:  # a branch's column by itself
+        fits = need[1] == 1
+    if not fits:
+        raise ValueError(f"ckv_scale must be float32 {list(need)} with adjacent columns, one scale per "
+                         + (f"block of {block} rows" if block > 1 else "row") + " and 128 columns")
     p.ckv_scale, p.ckv_scale_stride = _ptr(ckv_scale), int(ckv_scale.stride(0))
 
 
@@ -248,8 +255,8 @@ def make_params(q, ckv, krope, seq_lens, w_uk, w_uv, out, workspace=None, *, n_b
     p.d_c, p.d_rope, p.d_nope, p.d_v = int(ckv.shape[1]), int(krope.shape[1]), int(q.shape[2]) - int(krope.shape[1]), int(w_uv.shape[2])
     p.q, p.ckv, p.krope = _ptr(q), _ptr(ckv), _ptr(krope)
     p.ckv_stride, p.krope_stride = int(ckv.stride(0)), int(krope.stride(0))
-    _cache_format(p, ckv, ckv_scale, scale_block)
     p.cache_rows = int(ckv.shape[0]) if cache_rows is None else int(cache_rows)
+    _cache_format(p, ckv, ckv_scale, scale_block, p.cache_rows)
     p.seq_lens = _ptr(seq_lens)
     p.block_table = _ptr(block_table)
     p.max_pages = int(block_table.shape[1]) if block_table is not None else 0
@@ -434,7 +441,7 @@ def _cache_rows(p, ckv, krope, ckv_scale, scale_block: int) -> None:
     _rows_2d(ckv, p.d_c, ckv.dtype, "ckv")
     _rows_2d(krope, 64, torch.bfloat16, "krope")
     _need(int(krope.shape[0]) >= int(ckv.shape[0]), "krope has fewer rows than ckv")
-    _cache_format(p, ckv, ckv_scale, scale_block)
+    _cache_format(p, ckv, ckv_scale, scale_block, int(ckv.shape[0]))
     p.ckv, p.krope = _ptr(ckv), _ptr(krope)
     p.ckv_stride, p.krope_stride, p.cache_rows = int(ckv.stride(0)), int(krope.stride(0)), int(ckv.shape[0])
 

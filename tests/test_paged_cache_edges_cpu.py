@@ -1,0 +1,55 @@
+"""CPU tests of the paged cache's edges: buffers that are too small for what a call would read or
+write are refused in the binding."""
+import pytest
+import torch
+
+import head_rank_attention_b200 as hra
+
+BAD_SCALES = {
+    "short": torch.zeros(63, 2), "block_sized": torch.zeros(2, 2), "narrow": torch.zeros(64, 1), "half": torch.zeros(64, 2).half(),
+    "double": torch.zeros(64, 2).double(), "transposed": torch.zeros(2, 64).t(), "flat": torch.zeros(128),
+    "deep": torch.zeros(64, 2, 1), "none": None,
+}
+
+
+def _bf(*n):
+    return torch.zeros(*n, dtype=torch.bfloat16)
+
+
+def _i32(*n):
+    return torch.zeros(*n, dtype=torch.int32)
+
+
+@pytest.mark.parametrize("block", [0, 1])
+@pytest.mark.parametrize("name", BAD_SCALES)
+def test_scales_per_row_must_cover_the_cache(name, block):
+    """A scale tensor that the append would write past, or that is not what the pointer would say."""
+    ckv, krope, kw = torch.zeros(64, 256, dtype=torch.int8), _bf(64, 64), dict(ckv_scale=BAD_SCALES[name], scale_block=block)
+    with pytest.raises(ValueError, match="ckv_scale"):
+        hra.make_append_params(_bf(5, 256), _bf(5, 64), _i32(5), _i32(5), ckv, krope, **kw)
+    with pytest.raises(ValueError, match="ckv_scale"):
+        hra.make_load_params(ckv, krope, _i32(1), _bf(1, 7, 320), seq_stride=64, **kw)
+    w = _bf(8, 256, 128)
+    with pytest.raises(ValueError, match="ckv_scale"):
+        hra.make_params(_bf(1, 8, 192), ckv, krope, _i32(1), w, w, _bf(1, 8, 128), n_branch=2, seq_stride=64, **kw)
+
+
+@pytest.mark.parametrize("scale", [torch.zeros(64, 2), torch.zeros(70, 4)[:, 1:3], torch.zeros(64, 8)])
+def test_scales_per_row_that_cover_it(scale):
+    ckv, krope = torch.zeros(64, 256, dtype=torch.int8), _bf(64, 64)
+    p = hra.make_append_params(_bf(5, 256), _bf(5, 64), _i32(5), _i32(5), ckv, krope, ckv_scale=scale)
+    assert p.ckv_scale == scale.data_ptr() and p.ckv_scale_stride == scale.stride(0)
+    p = hra.make_load_params(ckv, krope, _i32(1), _bf(1, 7, 320), seq_stride=64, ckv_scale=scale, scale_block=1)
+    assert p.ckv_scale_stride == scale.stride(0)
+
+
+def test_scales_of_a_branch_and_of_a_part_of_the_rows():
+    """One branch's column, as a view or by itself; a decode that addresses fewer rows than the tensor has."""
+    w, ckv = _bf(8, 128, 128), torch.zeros(64, 128, dtype=torch.int8)
+    for scale in (torch.zeros(64, 4)[:, 2:3], torch.zeros(64)):
+        hra.make_params(_bf(1, 8, 192), ckv, _bf(64, 64), _i32(1), w, w, _bf(1, 8, 128), n_branch=1, seq_stride=64, ckv_scale=scale)
+    short = torch.zeros(40, 1)
+    hra.make_params(_bf(1, 8, 192), ckv, _bf(64, 64), _i32(1), w, w, _bf(1, 8, 128), n_branch=1, seq_stride=64, ckv_scale=short,
+                    cache_rows=40)
+    with pytest.raises(ValueError, match="ckv_scale"):
+        hra.make_params(_bf(1, 8, 192), ckv, _bf(64, 64), _i32(1), w, w, _bf(1, 8, 128), n_branch=1, seq_stride=64, ckv_scale=short)
