@@ -147,6 +147,8 @@ hra_status read_plan_status(const hra_plan_params* p, cudaStream_t stream) {
     case hra::kPlanTableFull: return fail(HRA_ERR_PLAN, "sequence %d needs more than max_pages pages", st[1]);
     case hra::kPlanTooManyTokens: return fail(HRA_ERR_PLAN, "%d new tokens, max_tokens=%d", st[2], st[3]);
     case hra::kPlanNoPages: return fail(HRA_ERR_PLAN, "%d pages needed, %d free", st[2], st[3]);
+    case hra::kPlanBadPage:
+      return fail(HRA_ERR_PLAN, "place %d of the ring of free pages holds %d, which is no page of the pool", st[2], st[3]);
     default: return fail(HRA_ERR_PLAN, "the free range does not describe a ring of num_pages pages (code %d)", st[0]);
   }
 }

@@ -73,10 +73,11 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
   __shared__ int len_s[kMaxBatch], have_s[kMaxBatch], start_s[kMaxBatch], take_s[kMaxBatch], give_s[kMaxBatch];
   __shared__ int bad_s;         // refusal code << 16 | sequence, the smallest
   __shared__ int ring_s[2];     // the ring's head and tail as places
+  __shared__ int alien_s;       // the first page to be taken that is none of the pool
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5, B = a.batch, P = a.page_size;
   const int n_warps = blockDim.x >> 5;
   grid_dep_wait();
-  if (t == 0) bad_s = INT_MAX;
+  if (t == 0) bad_s = alien_s = INT_MAX;
   __syncthreads();
   const bool mine = t < B;
   const int len = mine ? a.seq_lens[t] : 0;
@@ -110,6 +111,10 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
   if (t == 32) ring_s[0] = static_cast<int>(head >= 0 ? head % a.num_pages : 0);
   if (t == 64) ring_s[1] = static_cast<int>(tail >= 0 ? tail % a.num_pages : 0);
   __syncthreads();
+  const int head0 = ring_s[0], tail0 = ring_s[1];
+  auto place = [&](int from, int i) { return from + i < a.num_pages ? from + i : from + i - a.num_pages; };
+  // the first pages that may be taken, asked for ahead of the sums that say how many are
+  const int page0 = t < a.num_pages ? a.free_pages[place(head0, t)] : 0;
   unsigned long long wp = lane < n_warps ? sum_pages[lane] : 0, wt = lane < n_warps ? sum_tokens[lane] : 0;
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
@@ -140,8 +145,12 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
       limit = static_cast<int>(avail);
     }
   }
-  const bool ok = bad == INT_MAX;
-  const int n_tokens = ok ? static_cast<int>(tokens_total) : 0;
+  if (bad == INT_MAX) {  // every block looks at all pages to be taken: the step is refused as a whole
+    for (int i = t; i < need_total; i += blockDim.x) {
+      const int page = i == t ? page0 : a.free_pages[place(head0, i)];
+      if (page < 0 || page >= a.num_pages) atomicMin(&alien_s, i);
+    }
+  }
   if (mine) {
     len_s[t] = len;
     have_s[t] = have;
@@ -154,6 +163,13 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
   }
   __syncthreads();
+  if (alien_s != INT_MAX) {
+    bad = kPlanBadPage << 16;
+    wanted = place(head0, alien_s);
+    limit = a.free_pages[wanted];
+  }
+  const bool ok = bad == INT_MAX;
+  const int n_tokens = ok ? static_cast<int>(tokens_total) : 0;
   if (blockIdx.x == 0) {
     if (mine) {
       a.seq_lens_out[t] = ok ? static_cast<int>(after) : len;
@@ -170,8 +186,6 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
     }
   }
   const int threads = gridDim.x * blockDim.x, me = blockIdx.x * blockDim.x + t;
-  const int head0 = ring_s[0], tail0 = ring_s[1];
-  auto place = [&](int from, int i) { return from + i < a.num_pages ? from + i : from + i - a.num_pages; };
   if (ok) {
     // pages taken: the ring's next ones, in the order of the sequences
     for (int i = me; i < need_total; i += threads) {

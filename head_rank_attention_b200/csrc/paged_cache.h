@@ -52,6 +52,7 @@ enum PlanStatus : int {
   kPlanTooManyTokens = 3,  // status[2] = tokens asked for, status[3] = max_tokens
   kPlanNoPages = 4,        // status[2] = pages needed, status[3] = pages free
   kPlanBadPool = 5,        // the free range does not describe this pool
+  kPlanBadPage = 6,        // status[2] = place in the ring, status[3] = the page there, which is none of the pool
 };
 
 struct AppendArgs {  // see hra_append_params

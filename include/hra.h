@@ -279,7 +279,8 @@ HRA_API hra_status hra_check_prefill_status(const hra_prefill_params* p, void* s
  * left as it was).
  * A step that cannot be served is refused as a whole: lengths and pool stay as they were, no
  * page is taken or given back, every slot is -1, and status says why (hra_check_plan_status
- * reads it).  Slots and positions behind the last token are -1, so a captured step can be
+ * reads it).  A cached page that is none of the pool leaves its tokens without a slot (-1), and is given
+ * back unseen when its request ends: the step that would take it from the ring is refused.  Slots and positions behind the last token are -1, so a captured step can be
  * replayed with any number of tokens up to max_tokens.
  * seq_lens_out and free_range_out may be seq_lens and free_range themselves; no other buffers may
  * overlap.  With buffers of their own, the same call can be made again and gives the same plan.
@@ -302,7 +303,9 @@ typedef struct {
                                  negative or longer than its table row; 2 = sequence status[1]
                                  needs more than max_pages pages; 3 = status[2] tokens, over
                                  max_tokens; 4 = status[2] pages needed, status[3] free; 5 = the
-                                 free range does not describe a ring of num_pages pages     */
+                                 free range does not describe a ring of num_pages pages; 6 =
+                                 a page to be taken, at place status[2] of the ring, is
+                                 status[3] and no page of the pool                          */
 } hra_plan_params;
 
 HRA_API hra_status hra_page_plan(const hra_plan_params* p, void* stream /* cudaStream_t */);

@@ -122,6 +122,10 @@ def page_plan(lens, new, table, ring, free, page: int, max_tokens: int):
     if need > tail - head:
         out["status"] = [4, 0, need, tail - head]
         return out
+    for k in range(head, head + need):
+        if not 0 <= ring[k % n] < n:
+            out["status"] = [6, 0, k % n, int(ring[k % n])]
+            return out
     at = 0
     for b in range(B):
         if new[b] >= 0:

@@ -1,9 +1,11 @@
 """CPU tests of the paged cache's edges: buffers that are too small for what a call would read or
 write are refused in the binding."""
+import numpy as np
 import pytest
 import torch
 
 import head_rank_attention_b200 as hra
+from oracle import paged
 
 BAD_SCALES = {
     "short": torch.zeros(63, 2), "block_sized": torch.zeros(2, 2), "narrow": torch.zeros(64, 1), "half": torch.zeros(64, 2).half(),
@@ -53,3 +55,14 @@ def test_scales_of_a_branch_and_of_a_part_of_the_rows():
                     cache_rows=40)
     with pytest.raises(ValueError, match="ckv_scale"):
         hra.make_params(_bf(1, 8, 192), ckv, _bf(64, 64), _i32(1), w, w, _bf(1, 8, 128), n_branch=1, seq_stride=64, ckv_scale=short)
+
+
+@pytest.mark.parametrize("ring,status", [
+    ([2, -1, 3, 0], [6, 0, 1, -1]), ([4, 0, 1, 2], [6, 0, 0, 4]), ([0, 1, 2, -9], [0, 0, 0, 0])])
+def test_a_page_to_be_taken_that_is_none_of_the_pool(ring, status):
+    """Three pages are taken of the four: a step that met a bad one is refused as a whole."""
+    p = paged.page_plan([0, 31], [33, 2], np.array([[-1, -1], [7, -1]]), np.array(ring), [0, 4], 32, 64)
+    assert p["status"] == status
+    if status[0]:
+        assert (p["slots"] == -1).all() and p["free"] == [0, 4] and p["lens"].tolist() == [0, 31]
+        assert p["table"].tolist() == [[-1, -1], [7, -1]] and p["ring"].tolist() == ring
