@@ -64,7 +64,6 @@ __device__ __forceinline__ void store_q32(const AbsorbArgs& a, long long dst, co
 // grid (h, ceil(B / 128), max(d_c / 256, 1) latent parts), 256 threads, two CTAs per SM.
 // Warp w owns the sequences of TMEM lane quadrant w % 4 and 128 of the CTA's
 // min(d_c, 256) latent columns (w / 4; with 128 columns warps 4-7 only rotate q_rope).
-template <bool LATE>  // see launch_absorb_q's late_release
 __global__ void __launch_bounds__(AbsorbCfg::THREADS, 1)
 absorb_tc_kernel(const __grid_constant__ CUtensorMap map_wuk, const __grid_constant__ CUtensorMap map_q,
                  const AbsorbArgs a) {
@@ -84,7 +83,7 @@ absorb_tc_kernel(const __grid_constant__ CUtensorMap map_wuk, const __grid_const
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    if (!LATE) grid_dep_launch();
+    grid_dep_launch();
     mbar_init(&bars[0], 1);
     mbar_init(&bars[1], 1);
     *abort_flag = 0;
@@ -127,10 +126,6 @@ absorb_tc_kernel(const __grid_constant__ CUtensorMap map_wuk, const __grid_const
     }
     __syncwarp();
   }
-  // Everything above reads only inputs of the call; what follows writes the workspace,
-  // which the previous call's kernels read, so it waits for them.
-  grid_dep_wait();
-  if (LATE && threadIdx.x == 0) grid_dep_launch();
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && warp == 3)
     tile_prefix_warp(a.seq_lens, a.batch, a.tile_tokens, a.tile_prefix);
   const int r = 32 * (warp & 3) + lane;  // sequence within the chunk = TMEM lane
@@ -715,7 +710,6 @@ __global__ void __launch_bounds__(kSmallThreads, 2) combine_small_kernel(const C
 __global__ void __launch_bounds__(256) partial_combine_kernel(const CombineArgs a) {
   constexpr int CPT = 16;
   if (threadIdx.x == 0) grid_dep_launch();
-  grid_dep_wait();  // o_lat is read by the previous call's up-projection
   const int head = blockIdx.x * 32 + threadIdx.x / 8;
   const int col = (threadIdx.x % 8) * CPT;
   const int slice = blockIdx.y, seq = blockIdx.z, slices = gridDim.y;
@@ -777,13 +771,11 @@ int absorb_seq_chunk(int) { return 128; }
 int upproj_seq_chunk() { return 32; }
 
 cudaError_t launch_absorb_q(const CUtensorMap& map_wuk, const CUtensorMap& map_q, const AbsorbArgs& a,
-                            cudaStream_t stream, bool pdl, bool late_release) {
-  auto kern = late_release ? absorb_tc_kernel<true> : absorb_tc_kernel<false>;
-  cudaError_t e = set_smem(kern, AbsorbCfg::SMEM);
+                            cudaStream_t stream) {
+  cudaError_t e = set_smem(absorb_tc_kernel, AbsorbCfg::SMEM);
   if (e != cudaSuccess) return e;
-  return launch_kernel(kern, dim3(a.heads, (a.batch + 127) / 128, a.d_c > 256 ? a.d_c / 256 : 1),
-                       dim3(AbsorbCfg::THREADS),
-                       AbsorbCfg::SMEM, stream, pdl, map_wuk, map_q, a);
+  return launch_kernel(absorb_tc_kernel, dim3(a.heads, (a.batch + 127) / 128, a.d_c > 256 ? a.d_c / 256 : 1),
+                       dim3(AbsorbCfg::THREADS), AbsorbCfg::SMEM, stream, false, map_wuk, map_q, a);
 }
 
 cudaError_t launch_combine_upproj(const CUtensorMap& map_wuv, const CUtensorMap& map_olat, const CombineArgs& a,
@@ -820,7 +812,7 @@ cudaError_t launch_combine_upproj(const CUtensorMap& map_wuv, const CUtensorMap&
 cudaError_t launch_combine_partials(const CUtensorMap& map_wuv, const CUtensorMap& map_olat, const CombineArgs& a,
                                     cudaStream_t stream, bool pdl) {
   cudaError_t e = launch_kernel(partial_combine_kernel, dim3((a.heads + 31) / 32, a.d_c / 128, a.batch), dim3(256),
-                                0, stream, pdl, a);
+                                0, stream, false, a);
   if (e != cudaSuccess) return e;
   if ((e = set_smem(upproj_tc_kernel, UpprojCfg::SMEM)) != cudaSuccess) return e;
   return launch_kernel(upproj_tc_kernel, dim3(a.heads, (a.batch + 127) / 128), dim3(UpprojCfg::THREADS),

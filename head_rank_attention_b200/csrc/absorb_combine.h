@@ -57,12 +57,9 @@ int upproj_seq_chunk();
 
 // map_wuk: W_UK viewed as [h*d_c rows, 128] bf16, box {64, min(d_c, 256)}, SWIZZLE_128B.
 // map_q:   q viewed as [B rows, h*192] bf16, box {64, absorb_seq_chunk(B)}, SWIZZLE_128B.
-// pdl: launch with programmatic dependent launch (launch.h).
-// late_release: the decode kernel, which loads lengths, block table, scales and cache ahead of its own
-// wait, is started only once everything in front of this call is complete and visible (free with
-// block scales; without them 1 us at h = 16, so false there).
+// A call's first kernel: launched plainly (launch.h).
 cudaError_t launch_absorb_q(const CUtensorMap& map_wuk, const CUtensorMap& map_q, const AbsorbArgs& a,
-                            cudaStream_t stream, bool pdl, bool late_release);
+                            cudaStream_t stream);
 // Batches of up to kSmallBatch sequences with few heads take one fused merge + up-projection
 // kernel; the others the merge kernel and the tensor-core up-projection.
 constexpr int kSmallBatch = 4;

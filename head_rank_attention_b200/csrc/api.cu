@@ -278,10 +278,7 @@ hra_status run_decode(const hra_decode_params* p, cudaStream_t stream) {
   ab.tile_prefix = tile_prefix;
   ab.tile_tokens = hra::decode_tile_tokens(dc / p->n_branch, p->scale_block);
   ab.q_positions = p->q_positions;
-  // Programmatic dependent launch lets each kernel start while the previous one drains;
-  // the stage-timing mode launches plainly so that its events bracket whole kernels.
-  const bool pdl = p->stage_events == nullptr;
-  e = hra::launch_absorb_q(map_wuk, map_q, ab, stream, pdl, p->scale_block > 1);
+  e = hra::launch_absorb_q(map_wuk, map_q, ab, stream);
   if (e != cudaSuccess) return cuda_fail(e, "absorb_q launch");
 
   const float tau = p->softmax_scale > 0.f ? p->softmax_scale : 1.0f / std::sqrt(192.0f);
@@ -307,6 +304,9 @@ hra_status run_decode(const hra_decode_params* p, cudaStream_t stream) {
   da.ckv_scale = int8 ? p->ckv_scale : nullptr;
   da.scale_stride = int8 ? p->ckv_scale_stride : 0;
   if ((e = mark(1)) != cudaSuccess) return cuda_fail(e, "stage event");
+  // Programmatic dependent launch lets the call's other kernels start while the one before drains;
+  // the stage-timing mode launches plainly so that its events bracket whole kernels.
+  const bool pdl = p->stage_events == nullptr;
   e = hra::launch_decode_kernel(p->n_branch, map_ckv, map_krope, da, plan.groups, stream, pdl);
   if (e != cudaSuccess) return cuda_fail(e, "decode launch");
   if ((e = mark(2)) != cudaSuccess) return cuda_fail(e, "stage event");

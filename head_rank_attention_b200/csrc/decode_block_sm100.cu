@@ -490,9 +490,8 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
     regs_inc<C::SOFTMAX_REGS>();
-    // The query comes from the previous kernel, and the partials written here are read by
-    // the previous call's merge: wait for those grids.  The other roles touch no memory
-    // that another kernel of the chain writes.
+    // The query comes from the previous kernel: wait for it.  The other roles touch no memory that
+    // another kernel of the call writes.
     grid_dep_wait();
     const int b = warp >> 2;          // stream
     const int row = threadIdx.x & 127;  // head row == TMEM lane

@@ -335,8 +335,7 @@ decode_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_constant
     }
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
-    // The absorbed query comes from the previous kernel, and the split partials written
-    // here are read by the previous call's merge: wait for those grids.
+    // The absorbed query comes from the previous kernel: wait for it.
     grid_dep_wait();
     constexpr int HALF = C::HALF;
     const int half = warp >> 2;                        // which half of the score columns

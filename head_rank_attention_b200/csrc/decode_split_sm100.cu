@@ -435,9 +435,8 @@ decode_split_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
     }
   } else {
     // ------------------------------------------------------------------ softmax + epilogue
-    // The absorbed query comes from the previous kernel, and the split partials written
-    // here are read by the previous call's merge: wait for those grids.  The producer, the
-    // converters and the MMA issuers touch no memory another kernel writes.
+    // The absorbed query comes from the previous kernel: wait for it.  The producer, the
+    // converters and the MMA issuers touch no memory another kernel of the call writes.
     grid_dep_wait();
     const int half = warp >> 2;           // score columns [half*HALF, +HALF), O columns [64 half, +64)
     const int row = threadIdx.x & 127;    // head row == TMEM lane

@@ -1,15 +1,18 @@
 // launch.h -- kernel launches with programmatic dependent launch (PDL).
 //
 // A kernel launched with pdl = true may start while the previous kernel on the stream is
-// still running: its CTAs run their set-up (barriers, TMEM, loads of inputs no earlier
-// kernel writes) and then execute griddepcontrol.wait (grid_dep_wait in sm100.cuh), which
-// returns once the previous grid has completed and its writes are visible.  Every kernel
-// of the decode path therefore reads the outputs of earlier kernels, and writes anything
-// an earlier kernel reads, only after grid_dep_wait.  Each kernel also signals
-// griddepcontrol.launch_dependents early so that the next one can be scheduled.
-// The kernels that write later calls' inputs (paged_cache.cu) do not signal, and the first kernel of a
-// block-scaled decode and of a prefill does so only after its own wait: all that was in
-// front of the call is then complete for the call's other kernels.
+// still running: its CTAs run their set-up (barriers, TMEM, loads of the call's inputs) and then
+// execute griddepcontrol.wait (grid_dep_wait in sm100.cuh), which returns once the previous
+// grid has completed and its writes are visible.  Every kernel of a call therefore reads the
+// outputs of the call's earlier kernels, and writes anything they read, only after
+// grid_dep_wait.  Each kernel also signals griddepcontrol.launch_dependents early so that the
+// next one can be scheduled.
+// The first kernel of a decode, a prefill or a combination of partial states is launched plainly:
+// it starts when all that was queued before the call is complete and visible.  The call's other
+// kernels start after it has, so the inputs that they load ahead of their waits (lengths, block table,
+// cache, weights) are complete too, whichever kernel, this library's or not, wrote them.  It costs
+// nothing: the status word's memset in front of that kernel overlaps with no kernel either.
+// The one-kernel calls of the paged cache wait before they read anything.
 #pragma once
 
 #include <cuda_runtime.h>

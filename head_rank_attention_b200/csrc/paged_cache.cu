@@ -29,21 +29,9 @@ namespace {
 
 constexpr uint32_t kAll = 0xffffffffu;
 
-// What is written here are later calls' inputs, and decode and prefill load a call's inputs before
-// they wait for the kernels in front of them, behind a first kernel that waits in their place.  So no
-// kernel here signals early (no grid_dep_launch): the next one starts when every block has ended.
-// Where the call's first kernel starts the others only after its own wait (block-scaled decode:
-// launch_absorb_q's late_release; prefill) that is enough.  A decode of the other formats does not, so the
-// page plan and the append to them end each block with publish: its writes are in memory, for
-// TMA loads too (the barrier hands them to one thread's fences).  0.4 us; on every kernel it
-// would be 1.8 us for 24 k tokens of a branch and 4 for 160 k loaded rows.
-__device__ __forceinline__ void publish() {
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    asm volatile("fence.proxy.async.global;" ::: "memory");
-  }
-}
+// These kernels may start while the one in front drains, and wait for it before they read anything.
+// What they write is complete for whatever comes behind: another of them waits likewise, and a
+// decode, a prefill or a combination begins with a plain launch (launch.h).
 
 // An element's place, past 32 bits in a long cache.
 __device__ __forceinline__ long long wide(int row, int stride) { return static_cast<long long>(row) * stride; }
@@ -214,7 +202,6 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
     a.slots[i] = slot;
     if (a.positions != nullptr) a.positions[i] = pos;
   }
-  publish();
 }
 
 // ------------------------------------------------------------------------------- append
@@ -294,7 +281,6 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const A
   const int g = blockIdx.y, groups = a.d_c / 128;
   const int i0 = blockIdx.x * W, n_win = min(W, a.n_tokens - i0);
   const int rows = static_cast<int>(a.cache_rows);
-  const bool fenced = F == kCacheBf16 || a.scale_block == 1;  // see publish
   grid_dep_wait();
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.rows_out);
 
@@ -338,7 +324,6 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const A
         *reinterpret_cast<uint32_t*>(o + 32) = y2;
       }
     }
-    if (fenced) publish();
     return;
   }
 
@@ -500,7 +485,6 @@ __global__ void __launch_bounds__(kAppendThreads, 3) cache_append_kernel(const A
       __syncthreads();  // warp_max is written again
     }
   }
-  if (fenced) publish();
 }
 
 // --------------------------------------------------------------------------------- load

@@ -49,11 +49,8 @@ __global__ void prefill_prep_kernel(const PrefillArgs a) {
   __shared__ double turns[32];  // rotation pair d turns by theta^(-2d/64) / (2 pi) per position
   if (threadIdx.x < 32) turns[threadIdx.x] = pow(static_cast<double>(a.rope_theta), -2.0 * threadIdx.x / 64.0) *
                                              0.15915494309189535;
-  __syncthreads();
-  grid_dep_wait();  // q16 / kr16 are read by the previous call's attention
-  // Not before the wait: the expansion loads the latent ahead of its own wait, and a kernel in
-  // front of this call may be writing it.
   if (threadIdx.x == 0) grid_dep_launch();
+  __syncthreads();
   const int nq = a.n_query * a.heads;
   const long long total = static_cast<long long>(nq) + a.l_pad;
   for (long long r = blockIdx.x * static_cast<long long>(blockDim.x) + threadIdx.x; r < total;
@@ -187,7 +184,7 @@ prefill_expand_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_
     }
     __syncwarp();
   }
-  grid_dep_wait();  // K / V are read by the previous call's attention
+  grid_dep_wait();  // the attention waits for this kernel alone: it completes after the preparation
   const bool done = mbar_wait(done_bar, 0, kDrainNs, never_flag, a.status, 63);
   tc_fence_after();
   if (done && !*abort_flag) {
@@ -521,7 +518,7 @@ cudaError_t set_smem(K kern, int bytes) {
 }  // namespace
 
 cudaError_t launch_prefill(const PrefillMaps& m, const PrefillArgs& a, cudaStream_t stream) {
-  cudaError_t e = launch_kernel(prefill_prep_kernel, dim3(148 * 4), dim3(128), 0, stream, true, a);
+  cudaError_t e = launch_kernel(prefill_prep_kernel, dim3(148 * 4), dim3(128), 0, stream, false, a);
   if (e != cudaSuccess) return e;
   if ((e = set_smem(prefill_expand_kernel, ExpandCfg::SMEM)) != cudaSuccess) return e;
   e = launch_kernel(prefill_expand_kernel, dim3(a.l_pad / 128, a.heads, a.n_branch), dim3(ExpandCfg::THREADS),

@@ -35,9 +35,9 @@
  * The decode kernels convert each cache tile to fp16 in shared memory (exact for bf16
  * values of fp16's range) and score it against the absorbed query in fp16; the softmax
  * weights P are fp16 in the P.V product.  |cache values| must stay below 65504.
- * Stream order: the kernels of a call are chained with programmatic dependent launch, so
- * a call may begin (set-up, loads of its inputs) while the previous call on the stream
- * drains; it touches the workspace only once that call has completed.
+ * Stream order: a call reads and writes its buffers once everything queued before it on
+ * the stream is complete; the kernels within a call are chained with programmatic dependent
+ * launch.
  */
 #ifndef HRA_H
 #define HRA_H

@@ -50,3 +50,144 @@ def test_a_bad_page_given_back_is_not_handed_out():
     plan.new.copy_(torch.tensor([64, 0]))
     hra.page_plan(plan.p)
     assert plan.status.tolist() == [6, 0, 3, 9] and plan.free.tolist() == [2, 4] and plan.lens.tolist() == [0, 64]
+
+
+# ------------------------------------------------- chains of calls with nothing between them
+def _bf16(r, *shape, std=1.0):
+    return torch.tensor(r.standard_normal(shape) * std, dtype=torch.bfloat16, device="cuda")
+
+
+def _i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+class Chain:
+    """Steps that write the same buffers in turn, each ending in an output of its own: queued with
+    nothing between the calls, in a stream or a captured graph, they give bit for bit what they give when
+    every call is waited for (no sum's order depends on timing)."""
+
+    def __init__(self):
+        self.steps = []  # (calls, output)
+
+    def add(self, calls, out):
+        self.steps.append((calls, out))
+
+    def queue(self, wait):
+        outs = []
+        for calls, out in self.steps:
+            for call in calls:
+                call()
+                if wait:
+                    torch.cuda.synchronize()
+            outs.append(out.clone())
+        return outs
+
+    def check(self, graph):
+        want = self.queue(True)
+        assert all(torch.isfinite(w).all() and w.abs().max() > 0 for w in want)
+        assert not torch.equal(want[0], want[1])
+        if graph:
+            g = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(g):
+                turns = [self.queue(False) for _ in range(4)]
+            g.replay()
+        else:
+            torch.cuda.synchronize()
+            turns = [self.queue(False) for _ in range(4)]
+        torch.cuda.synchronize()
+        for got in turns:
+            for k, (g, w) in enumerate(zip(got, want)):
+                assert torch.equal(g, w), k
+
+
+def _plain_decode(r, rows, lens, n_branch, h=16):
+    """A bf16 decode over rows [B, L, 576] as they lie; returns its call and its output."""
+    B, L = rows.shape[:2]
+    q, w_uk, w_uv = _bf16(r, B, h, 192), _bf16(r, h, 512, 128, std=128 ** -0.5), _bf16(r, h, 512, 128, std=128 ** -0.5)
+    out = torch.zeros(B, h, 128, device="cuda")
+    flat = rows.view(B * L, 576)
+    p = hra.make_params(q, flat[:, :512], flat[:, 512:], lens, w_uk, w_uv, out, n_branch=n_branch, seq_stride=L)
+    keep = (q, w_uk, w_uv, rows, lens, hra.alloc_workspace(p))
+    return lambda: (hra.mlra_decode(p), keep)[0], out
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("n_branch", [1, 2, 4])
+def test_load_then_plain_decode(n_branch, graph):
+    """Rows of two 8-bit caches loaded in turn into one buffer, each read at once by a bf16 decode."""
+    r = np.random.default_rng(n_branch)
+    L, chain = 3000, Chain()
+    lens = _i32([L, 1777])
+    loaded = torch.zeros(2, L, 576, dtype=torch.bfloat16, device="cuda")
+    decode, out = _plain_decode(r, loaded, lens, n_branch)
+    for _ in range(2):
+        codes = torch.tensor(r.integers(-127, 128, (2 * L, 512)), dtype=torch.int8, device="cuda")
+        scale = torch.tensor(r.random((-(-2 * L // 32), 4)) / 64 + 1e-3, dtype=torch.float32, device="cuda")
+        krope = _bf16(r, 2 * L, 64)
+        p = hra.make_load_params(codes, krope, lens, loaded, seq_stride=L, ckv_scale=scale, scale_block=32)
+        p.keep = (codes, scale, krope)
+        chain.add([lambda p=p: hra.cache_load(p), decode], out)
+    chain.check(graph)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_rows_of_an_append_then_plain_decode(fmt, graph):
+    """The rows that a block-scaled append leaves, read at once by a bf16 decode."""
+    r = np.random.default_rng(11)
+    L, chain = 4096, Chain()
+    seen = torch.zeros(1, L, 576, dtype=torch.bfloat16, device="cuda")
+    decode, out = _plain_decode(r, seen, _i32([L]), 4)
+    codes = torch.zeros(L, 512, dtype={"int8": torch.int8, "e4m3": torch.float8_e4m3fn}[fmt], device="cuda")
+    krope, scale, slots = _bf16(r, L, 64), torch.zeros(L // 64, 4, device="cuda"), torch.arange(L, dtype=torch.int32, device="cuda")
+    for _ in range(2):
+        rows = _bf16(r, L, 576)
+        p = hra.make_append_params(rows[:, :512], rows[:, 512:], slots, slots, codes, krope, ckv_scale=scale, scale_block=64,
+                                   rows_out=seen[0])
+        p.keep = rows
+        chain.add([lambda p=p: hra.cache_append(p), decode], out)
+    chain.check(graph)
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_plan_append_decode_with_a_scale_per_row(graph):
+    r = np.random.default_rng(12)
+    page, wide, h, most, chain = 64, 100, 16, 9000, Chain()
+    zeros = lambda *n: torch.zeros(*n, dtype=torch.int32, device="cuda")  # noqa: E731
+    codes = torch.zeros(2 * wide * page, 512, dtype=torch.int8, device="cuda")
+    krope, scale = _bf16(r, 2 * wide * page, 64), torch.zeros(2 * wide * page, 4, device="cuda")
+    lens, lens_out, table, start, status, slots, positions = (zeros(2), zeros(2), zeros(2, wide), zeros(3), zeros(4), zeros(most),
+                                                              zeros(most))
+    ring = torch.arange(2 * wide, dtype=torch.int32, device="cuda")
+    free, free_out = (torch.tensor([0, 2 * wide], dtype=torch.int64, device="cuda") for _ in range(2))
+    q, w_uk, w_uv = _bf16(r, 2, h, 192), _bf16(r, h, 512, 128, std=128 ** -0.5), _bf16(r, h, 512, 128, std=128 ** -0.5)
+    out = torch.zeros(2, h, 128, device="cuda")
+    dec = hra.make_params(q, codes, krope, lens_out, w_uk, w_uv, out, n_branch=4, block_table=table, page_size=page, ckv_scale=scale)
+    keep = hra.alloc_workspace(dec)
+    for asks in ((4000, 5000), (6000, 3), (7, 6400)):
+        rows, new = _bf16(r, most, 576), _i32(asks)
+        plan = hra.make_plan_params(lens, new, table, ring, free, lens_out, free_out, start, slots, status, positions=positions,
+                                    page_size=page)
+        put = hra.make_append_params(rows[:, :512], rows[:, 512:], slots, positions, codes, krope, ckv_scale=scale)
+        plan.keep, put.keep = new, rows
+        chain.add([lambda p=plan: hra.page_plan(p), lambda p=put: hra.cache_append(p), lambda: hra.mlra_decode(dec)], out)
+    chain.check(graph)
+    del keep
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_inputs_written_just_before_a_call(graph):
+    """A decode whose query, lengths, table and cache a copy has only just written."""
+    r = np.random.default_rng(13)
+    chain, h, page = Chain(), 16, 64
+    sets = [dict(q=_bf16(r, 3, h, 192), lens=_i32(n), table=_i32(r.permutation(96).reshape(3, 32)),
+                 cache=_bf16(r, 96 * page, 576)) for n in ([2000, 1, 640], [65, 2048, 1500])]
+    live = {k: torch.zeros_like(v) for k, v in sets[0].items()}
+    w_uk, w_uv, out = _bf16(r, h, 512, 128, std=128 ** -0.5), _bf16(r, h, 512, 128, std=128 ** -0.5), torch.zeros(3, h, 128, device="cuda")
+    p = hra.make_params(live["q"], live["cache"][:, :512], live["cache"][:, 512:], live["lens"], w_uk, w_uv, out, n_branch=4,
+                        block_table=live["table"], page_size=page)
+    keep = hra.alloc_workspace(p)
+    for s in sets:
+        chain.add([lambda s=s: [live[k].copy_(v) for k, v in s.items()], lambda: hra.mlra_decode(p)], out)
+    chain.check(graph)
+    del keep
