@@ -22,6 +22,7 @@ HRA_F32 = 1
 HRA_INT8 = 2
 HRA_E4M3 = 3
 HRA_ERR_PLAN = -6
+HRA_VERSION = "0.2.0"  # of the header whose structs are mirrored below
 
 STATUS_NAMES = {0: "HRA_OK", -1: "HRA_ERR_INVALID_ARG", -2: "HRA_ERR_UNSUPPORTED", -3: "HRA_ERR_WORKSPACE",
                 -4: "HRA_ERR_CUDA", -5: "HRA_ERR_DEVICE_TIMEOUT", -6: "HRA_ERR_PLAN"}
@@ -129,6 +130,11 @@ def load_library() -> ctypes.CDLL:
     if not LIB_PATH.exists():
         raise ImportError(f"{LIB_PATH} is not built; run `python -m head_rank_attention_b200.build`")
     lib = ctypes.CDLL(str(LIB_PATH))
+    lib.hra_version.argtypes = []
+    lib.hra_version.restype = ctypes.c_char_p
+    built = lib.hra_version().decode()
+    if built.split()[1:2] != [HRA_VERSION]:  # it would read other fields than the structs above have
+        raise ImportError(f"{LIB_PATH} is {built}, not {HRA_VERSION}; run `python -m head_rank_attention_b200.build`")
     P = ctypes.POINTER(HraDecodeParams)
     lib.hra_workspace_size.argtypes = [P]
     lib.hra_workspace_size.restype = ctypes.c_size_t
@@ -151,8 +157,6 @@ def load_library() -> ctypes.CDLL:
     lib.hra_selftest_wait_timeout.restype = ctypes.c_int
     lib.hra_last_error.argtypes = []
     lib.hra_last_error.restype = ctypes.c_char_p
-    lib.hra_version.argtypes = []
-    lib.hra_version.restype = ctypes.c_char_p
     _lib = lib
     return lib
 

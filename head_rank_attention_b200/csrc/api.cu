@@ -613,6 +613,6 @@ hra_status hra_selftest_wait_timeout(void* workspace, int limit_us, void* stream
 
 const char* hra_last_error(void) { return g_last_error.c_str(); }
 
-const char* hra_version(void) { return "hra 0.1.0 (sm_100a)"; }
+const char* hra_version(void) { return "hra " HRA_VERSION " (sm_100a)"; }
 
 }  // extern "C"

@@ -42,6 +42,12 @@
 #ifndef HRA_H
 #define HRA_H
 
+/* The parameter structs carry no size: a call reads every field that the library's own header
+ * declares, whichever options are in use.  New versions add fields at the ends (0.2.0:
+ * hra_decode_params.scale_block), so a program compiled against another version's header has to
+ * be compiled again; comparing HRA_VERSION with hra_version() at start-up shows it. */
+#define HRA_VERSION "0.2.0"
+
 #include <stddef.h>
 #include <stdint.h>
 
@@ -395,7 +401,7 @@ HRA_API hra_status hra_selftest_wait_timeout(void* workspace, int limit_us, void
 /* Message describing the last error on this thread ("" if none). */
 HRA_API const char* hra_last_error(void);
 
-/* Library version string. */
+/* Library version string, "hra " HRA_VERSION " (sm_100a)" of the header it was built from. */
 HRA_API const char* hra_version(void);
 
 #ifdef __cplusplus

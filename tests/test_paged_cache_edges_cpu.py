@@ -1,10 +1,16 @@
 """CPU tests of the paged cache's edges: buffers that are too small for what a call would read or
-write are refused in the binding."""
+write are refused in the binding, pages that are none of the pool in the plan, and a library of
+another version's structs on loading."""
+import pathlib
+import re
+import subprocess
+
 import numpy as np
 import pytest
 import torch
 
 import head_rank_attention_b200 as hra
+from head_rank_attention_b200 import _binding as B
 from oracle import paged
 
 BAD_SCALES = {
@@ -66,3 +72,16 @@ def test_a_page_to_be_taken_that_is_none_of_the_pool(ring, status):
     if status[0]:
         assert (p["slots"] == -1).all() and p["free"] == [0, 4] and p["lens"].tolist() == [0, 31]
         assert p["table"].tolist() == [[-1, -1], [7, -1]] and p["ring"].tolist() == ring
+
+
+def test_versions_of_header_library_and_binding_agree(tmp_path, monkeypatch):
+    header = (pathlib.Path(__file__).resolve().parents[1] / "include" / "hra.h").read_text()
+    declared = re.search(r'#define HRA_VERSION "([^"]+)"', header).group(1)
+    assert declared == B.HRA_VERSION and hra.version() == f"hra {declared} (sm_100a)"
+    src, lib = tmp_path / "other.c", tmp_path / "libother.so"
+    src.write_text('const char* hra_version(void) { return "hra 0.1.0 (sm_100a)"; }\n')
+    subprocess.run(["gcc", "-shared", "-fPIC", str(src), "-o", str(lib)], check=True)
+    monkeypatch.setattr(B, "LIB_PATH", lib)
+    monkeypatch.setattr(B, "_lib", None)
+    with pytest.raises(ImportError, match="0.1.0"):
+        B.load_library()
