@@ -319,7 +319,7 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
       bool ok = true;
       for (int it0 = 0; ok && it0 < ntiles; it0 += TPB) {
         // this lane's chunk: s = f * 2^e
-        const uint32_t bits = __float_as_uint(scale);
+        const uint32_t bits = __float_as_uint(scale == 0.f ? 0.f : scale);  // -0 is no negative scale
         const int ex = static_cast<int>(bits >> 23) - 127;  // s >= 0
         const bool none = bits < 0x00800000u;                 // zero (or subnormal: taken as zero)
         const bool bad = bits >= 0x7F800000u;                 // Inf, NaN (or negative)

@@ -88,6 +88,17 @@ def test_a_bad_scale_passes_the_combination_of_ranges(heads, where):
     assert (out == 0).all()
 
 
+@pytest.mark.parametrize("zero", [0.0, -0.0])
+def test_zero_scales(zero):
+    """Blocks of scale 0 of either sign, beside others and as all that a sequence has: their codes stand for 0."""
+    wl = _case("zero", (300, 60), page_size=64)
+    inp = synth.make_inputs(wl)
+    codes, scale = _quantize(inp.cache[:, :512], 64, "int8")
+    for s, c, b in ((0, 1, 2), (0, 4, 0), (1, 0, 3)):
+        scale[int(inp.block_table[s, c]), b] = zero
+    assert_parity(_run(inp, wl, codes, scale, 64), _oracle(inp, wl, codes, scale, 64), "zero scales")
+
+
 # --------------------------------------------------------------------- scales far apart
 def _far_blocks(B, L, apart, high):
     """A paged case of 32-row blocks whose latents are 2^high, 2^(high - apart), 2^high, ... in size."""
