@@ -92,9 +92,13 @@ __device__ __forceinline__ uint32_t quantize4_exact(float4 x, float s) {
 
 // The same with fp32 arithmetic, for scales in [2^-90, 2^100] (quantize_fast_scale).
 //
-// kAnyScale: x * (1 / s) with one correction by its residual rounds as a division would, and where
-// that is a tie (all of the tie's bits zero), the sign of the new residual, exact in an FMA,
-// says on which side of it x / s lies.
+// kAnyScale: y = x * fl(1 / s) is within 1.5 units in the last place of Q = x / s; one correction by the
+// residual, q = fl(y + fl(x - y s) * fl(1 / s)), rounds Q + d with |d| below 2^-21 units.  So q is within a
+// unit of Q, and if q is no tie it lies on Q's side of every tie (a tie T is an fp32 number: Q < T < q
+// would be more than a unit apart).  Where q is a tie (all of the tie's bits zero) the new residual
+// x - q s, at most 0.6 units of q times s and so exact in an FMA, says by its sign on which side Q lies.
+// Nothing here needs q to be the correctly rounded quotient.  In the range of scales above no residual
+// of a quotient that matters (2^-10 and up) falls under fp32's smallest number.
 //
 // A scale that is fl32(amax / top) of a bf16 amax needs less.  With 8-bit significands X of x and A of
 // amax, top x / amax is top X / A times a power of two, which is a tie or at least 2^-16 of itself

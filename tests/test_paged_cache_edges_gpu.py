@@ -191,3 +191,33 @@ def test_inputs_written_just_before_a_call(graph):
         chain.add([lambda s=s: [live[k].copy_(v) for k, v in s.items()], lambda: hra.mlra_decode(p)], out)
     chain.check(graph)
     del keep
+
+
+# ------------------------------------------------------------------------------- append
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("rows", [1, 20])
+def test_quotients_by_a_scale_that_is_not_the_rows_own(fmt, rows):
+    """Open blocks of any scale: the nearest code to the exact quotient, for values on a border
+    between two codes, the neighbours of such values in bf16, and any others.  A quotient is a
+    border or 2^-33 of itself away from it, so its rounding to 64 bits keeps the side."""
+    r = np.random.default_rng(rows)
+    blocks, block = 600, 32
+    scale = np.ldexp(r.uniform(1, 2, blocks), r.integers(-85, 90, blocks))
+    scale[::3] = np.ldexp(r.integers(1, 128, len(scale[::3])), r.integers(-85, 84, len(scale[::3])))  # borders that are bf16
+    scale = scale.astype(np.float32)
+    grid = np.arange(128.0) if fmt == "int8" else paged.e4m3_values()
+    borders = (grid[1:] + grid[:-1]) / 2
+    borders = borders[borders * (1 + 2.0 ** -6) < paged.TOP[fmt]]  # the scale stays the block's
+    x = r.choice(borders, (blocks * rows, 128)) * r.choice([-1, 1], (blocks * rows, 128))
+    x[:, 96:] = r.uniform(-0.98, 0.98, (blocks * rows, 32)) * paged.TOP[fmt]
+    x = torch.tensor(x * np.repeat(scale.astype(np.float64), rows)[:, None], dtype=torch.bfloat16)
+    step = torch.tensor(r.integers(-1, 2, x.shape), dtype=torch.int16)
+    x = (x.view(torch.int16) + step).view(torch.bfloat16)  # the bf16 number itself, or a neighbour
+    want = paged.nearest(x.double().numpy() / np.repeat(scale.astype(np.float64), rows)[:, None], fmt)
+    slots = (np.arange(blocks)[:, None] * block + 1 + np.arange(rows)).reshape(-1)
+    codes = torch.zeros(blocks * block, 128, dtype={"int8": torch.int8, "e4m3": torch.float8_e4m3fn}[fmt], device="cuda")
+    krope, sd, s = torch.zeros(blocks * block, 64, dtype=torch.bfloat16, device="cuda"), torch.tensor(scale[:, None], device="cuda"), _i32(slots)
+    hra.cache_append(hra.make_append_params(x.cuda(), torch.zeros(len(slots), 64, dtype=torch.bfloat16, device="cuda"), s, s, codes,
+                                            krope, ckv_scale=sd, scale_block=block))
+    assert np.array_equal(sd.cpu().numpy()[:, 0], scale)
+    assert np.array_equal(codes.float().double().cpu().numpy()[slots], want)
