@@ -221,3 +221,47 @@ def test_quotients_by_a_scale_that_is_not_the_rows_own(fmt, rows):
                                             krope, ckv_scale=sd, scale_block=block))
     assert np.array_equal(sd.cpu().numpy()[:, 0], scale)
     assert np.array_equal(codes.float().double().cpu().numpy()[slots], want)
+
+
+# --------------------------------------------------------------------------- two streams
+def test_appends_and_loads_of_two_streams_overlap():
+    """Two caches, a stream each: appends that start every block anew and loads of what they wrote,
+    queued in turn on both streams with no wait between them."""
+    r = np.random.default_rng(21)
+    sides = []
+    for fmt, block, n in (("int8", 64, 12000), ("e4m3", 32, 9000)):
+        rows = -(-n // 64) * 64
+        codes = torch.zeros(rows, 512, dtype={"int8": torch.int8, "e4m3": torch.float8_e4m3fn}[fmt], device="cuda")
+        scale, krope = torch.zeros(rows // block, 4, device="cuda"), torch.zeros(rows, 64, dtype=torch.bfloat16, device="cuda")
+        slots, lens = torch.arange(n, dtype=torch.int32, device="cuda"), _i32([n])
+        stream, steps = torch.cuda.Stream(), []
+        for _ in range(6):
+            x = _bf16(r, n, 576)
+            seen, back = (torch.zeros(n, 576, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+            steps.append((hra.make_append_params(x[:, :512], x[:, 512:], slots, slots, codes, krope, ckv_scale=scale,
+                                                 scale_block=block, rows_out=seen),
+                          hra.make_load_params(codes, krope, lens, back[None], seq_stride=rows, ckv_scale=scale, scale_block=block),
+                          x, seen, back))
+        sides.append((stream, steps, (codes, scale, krope, slots, lens), fmt, block))
+    torch.cuda.synchronize()
+    for k in range(6):
+        for stream, steps, _, _, _ in sides:
+            hra.cache_append(steps[k][0], stream)
+            hra.cache_load(steps[k][1], stream)
+    torch.cuda.synchronize()
+    for _, steps, keep, fmt, block in sides:
+        for _, _, x, seen, back in steps:
+            assert torch.equal(seen, back)
+        # the last step's cache against the definition, and every step's rows near its own tokens
+        n = len(keep[3])
+        for _, _, x, seen, _ in steps:
+            top, eps = (127.0, 0.5 / 127) if fmt == "int8" else (448.0, 2.0 ** -4)
+            amax = torch.nn.functional.pad(x[:, :512].float().abs(), (0, 0, 0, -n % block)).view(-1, block, 4, 128).amax((1, 3))
+            a = amax.repeat_interleave(block, 0)[:n].repeat_interleave(128, 1)
+            # int8: half a step of amax / 127; e4m3: 2^-4 of the value or half a step of 2^-9 amax / 448; and bf16
+            off = a * eps if fmt == "int8" else torch.maximum(x[:, :512].float().abs() * eps, a * 2.0 ** -10 / 448)
+            assert ((seen[:, :512].float() - x[:, :512].float()).abs() <= off * 1.001 + 2.0 ** -8 * seen[:, :512].float().abs()).all()
+        want = paged.append(np.zeros((len(keep[0]), 512)), np.zeros(keep[1].shape, np.float32), np.zeros((len(keep[0]), 64)),
+                            steps[-1][2][:, :512].double().cpu().numpy(), steps[-1][2][:, 512:].double().cpu().numpy(),
+                            range(n), range(n), block, fmt)
+        assert np.array_equal(keep[0].float().double().cpu().numpy(), want[0]) and np.array_equal(keep[1].cpu().numpy(), want[1])
