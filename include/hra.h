@@ -329,7 +329,10 @@ HRA_API hra_status hra_check_plan_status(const hra_plan_params* p, void* stream)
  * Blocks grow: a call that writes row 0 of a block starts it anew; one that writes later rows
  * only keeps the larger of the block's scale and its own tokens', and where that is larger
  * than the block's was, the rows before the call's first one are brought to it (code' = the
- * nearest to code * s_old / s).  Rows behind the call's last are left as they were.
+ * nearest to code * s_old / s).  Each growth rounds them again, by half a step of the scale of the
+ * time: after g growths an int8 value is within (g + 1) / 2 scales of its latent, where a block written
+ * at once is within 1 / 2 (HRA_E4M3: 2^-4 of the value each time, or half of 2^-9 scales).  Rows behind
+ * the call's last are left as they were.
  * The tokens of one block follow one another in the call, and no slot comes twice (their
  * rows would hold parts of either; a block in two places of the call gets either's scale).
  * A latent that is no finite number makes its block's scale no finite number.
@@ -363,7 +366,7 @@ HRA_API hra_status hra_cache_append(const hra_append_params* p, void* stream /* 
 /*
  * Load: the cached rows of each sequence back as contiguous bf16 rows [C_KV | K_RoPE], the form
  * mlra_prefill reads: out[b, t] for t < min(seq_lens[b], max_tokens), 8-bit latents as
- * code * scale rounded once to bf16.  Rows behind a sequence's last are left as they were; a row whose
+ * code * scale in fp32, rounded to bf16.  Rows behind a sequence's last are left as they were; a row whose
  * page is not in the cache is zero.  The cache is described as in hra_decode_params.
  * d_c in {128, 256, 512}, d_rope = 64; 1 <= batch <= 1024; 1 <= max_tokens <= 2^30.  out 16-byte aligned, its strides
  * multiples of 8.  One launch, no workspace.

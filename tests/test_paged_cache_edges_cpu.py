@@ -85,3 +85,31 @@ def test_versions_of_header_library_and_binding_agree(tmp_path, monkeypatch):
     monkeypatch.setattr(B, "_lib", None)
     with pytest.raises(ImportError, match="0.1.0"):
         B.load_library()
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("growth", [0.0, 0.01, 0.3, 1.0])
+def test_how_far_a_growing_block_takes_its_values(fmt, growth):
+    """A block filled token by token, whose scale grows with nearly every token or not at all.  Every
+    growth rounds the earlier codes again: an int8 value moves by half a step of the scale of the
+    time, an e4m3 value by 2^-4 of itself or half a step of 2^-9 scales.  After g growths an int8
+    value is within (g + 1) / 2 of the scale from its latent."""
+    r = np.random.default_rng(17)
+    n = 64
+    x = r.standard_normal((n, 128)) * (1 + growth) ** np.arange(n)[:, None]
+    codes, s, off, grown = np.zeros((n, 128)), np.float32(0), np.zeros((n, 128)), np.zeros(n)
+    for t in range(n):
+        before = s
+        codes, s = paged.append_block(codes, s, x[t:t + 1], [t], fmt)
+        rounded = slice(0, t + 1) if s > before else slice(t, t + 1)
+        if s > before:
+            grown[:t] += 1
+        half = np.full_like(off[rounded], s / 2.0) if fmt == "int8" else np.maximum(
+            2.0 ** -4 * (np.abs(x[rounded]) + off[rounded]), 2.0 ** -10 * s)
+        off[rounded] += half
+    err = np.abs(codes * np.float64(s) - x)
+    # a scale is fl32(amax / top): the largest value may sit 2^-24 beyond the last code
+    assert (err <= off + 2.0 ** -23 * np.abs(x)).all()
+    assert grown.max() > (30 if growth >= 0.3 else 0)
+    if fmt == "int8":
+        assert (err <= ((grown + 1) / 2)[:, None] * s * (1 + 2.0 ** -20)).all()
