@@ -6,6 +6,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -212,6 +213,20 @@ hra_status encode_map(CUtensorMap* map, const void* base, int64_t inner, int64_t
   return HRA_OK;
 }
 
+hra_status check_block_kernel() {
+  static std::atomic<bool> known_good{false};
+  if (known_good.load(std::memory_order_relaxed)) return HRA_OK;
+  int have = 0, need = 0;
+  cudaError_t e = hra::decode_block_registers(&have, &need);
+  if (e != cudaSuccess) return cuda_fail(e, "block-scaled decode kernel");
+  if (have != need)
+    return fail(HRA_ERR_UNSUPPORTED,
+                "this build's block-scaled decode kernel has %d registers a thread and needs %d (csrc/decode_block_sm100.cu, "
+                "LAUNCH_REGS); it was compiled by another nvcc than it was written for", have, need);
+  known_good.store(true, std::memory_order_relaxed);
+  return HRA_OK;
+}
+
 hra_status run_decode(const hra_decode_params* p, cudaStream_t stream) {
   hra_status st = validate(p);
   if (st != HRA_OK) return st;
@@ -223,6 +238,7 @@ hra_status run_decode(const hra_decode_params* p, cudaStream_t stream) {
     return fail(HRA_ERR_WORKSPACE, "workspace is not 256-byte aligned");
   if (p->workspace_bytes < plan.total)
     return fail(HRA_ERR_WORKSPACE, "workspace_bytes=%zu < required %zu", p->workspace_bytes, plan.total);
+  if (p->scale_block > 1 && (st = check_block_kernel()) != HRA_OK) return st;
 
   uint8_t* ws = static_cast<uint8_t*>(p->workspace);
   int* status = reinterpret_cast<int*>(ws);

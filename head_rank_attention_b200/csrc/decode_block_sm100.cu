@@ -693,18 +693,23 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
 
 int decode_block_tile_tokens() { return BlockCfg::NT; }
 
+// The softmax warps' setmaxnreg waits for registers that a launch with fewer would not have.  128 is
+// the most that 512 threads can have and what the compiler takes; a build with another number is
+// refused, not tried.
+cudaError_t decode_block_registers(int* have, int* need) {
+  *have = 0;
+  *need = BlockCfg::LAUNCH_REGS;
+  cudaFuncAttributes i8{}, f8{};
+  cudaError_t e = cudaFuncGetAttributes(&i8, decode_block_kernel<false>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&f8, decode_block_kernel<true>);
+  if (e == cudaSuccess) *have = i8.numRegs < f8.numRegs ? i8.numRegs : f8.numRegs;
+  return e;
+}
+
 cudaError_t launch_decode_block_kernel(const CUtensorMap& map_ckv, const CUtensorMap& map_krope, const DecodeArgs& a,
                                        int groups, cudaStream_t stream, bool pdl) {
   using C = BlockCfg;
   auto kern = a.cache_int8 == 2 ? decode_block_kernel<true> : decode_block_kernel<false>;
-  // The softmax warps' setmaxnreg waits for registers that a launch with fewer would not have.
-  static const bool regs_ok = [] {
-    cudaFuncAttributes i8{}, f8{};
-    return cudaFuncGetAttributes(&i8, decode_block_kernel<false>) == cudaSuccess &&
-           cudaFuncGetAttributes(&f8, decode_block_kernel<true>) == cudaSuccess && i8.numRegs == C::LAUNCH_REGS &&
-           f8.numRegs == C::LAUNCH_REGS;
-  }();
-  if (!regs_ok) return cudaErrorInvalidKernelImage;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
   if (e != cudaSuccess) return e;
   return launch_kernel(kern, dim3(a.d_c / 128, groups), dim3(C::THREADS), C::SMEM_BYTES, stream, pdl, map_ckv,

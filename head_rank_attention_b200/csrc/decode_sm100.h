@@ -74,6 +74,10 @@ cudaError_t launch_decode_split_kernel(const CUtensorMap& map_ckv, const CUtenso
 cudaError_t launch_decode_block_kernel(const CUtensorMap& map_ckv, const CUtensorMap& map_krope,
                                        const DecodeArgs& a, int groups, cudaStream_t stream, bool pdl);
 
+// The registers a thread that it was built with, and the number that its launch needs: the caller
+// compares them before the first launch.
+cudaError_t decode_block_registers(int* have, int* need);
+
 // Launch the decode kernel on grid (d_c / 128 slices, `groups` KV splits); pdl:
 // programmatic dependent launch (launch.h).  Branches 128 wide run the split kernel, 256
 // and 512 wide the converting kernel.
