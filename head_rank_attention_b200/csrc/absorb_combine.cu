@@ -256,7 +256,7 @@ __global__ void __launch_bounds__(256 * Z) merge_kernel(const CombineArgs a) {
         // a group with an empty tile range (more groups than tiles) wrote nothing
         const bool live = g <= g_hi && group_live(g, G, T);
         const long long row = ((static_cast<long long>(g) + seq) * gridDim.y + slice) * 128 + head;
-        ml[u] = live ? partial_state(a.ml_part[row]) : make_float2(-INFINITY, 0.f);
+        ml[u] = live ? a.ml_part[row] : make_float2(-INFINITY, 0.f);
 #pragma unroll
         for (int v = 0; v < V; ++v)
           o[u][v] = live ? *reinterpret_cast<const float4*>(a.o_part + row * 128 + col + 4 * v)
@@ -264,7 +264,10 @@ __global__ void __launch_bounds__(256 * Z) merge_kernel(const CombineArgs a) {
       }
       float mx = M;
 #pragma unroll
-      for (int u = 0; u < GU; ++u) mx = fmaxf(mx, ml[u].x);
+      for (int u = 0; u < GU; ++u) {
+        ml[u] = partial_state(ml[u]);  // behind the loads: at each of them it would hold up the next
+        mx = fmaxf(mx, ml[u].x);
+      }
       if (mx != -INFINITY) {
         const float r = exp2f(M - mx);
         den *= r;
@@ -617,11 +620,12 @@ __global__ void __launch_bounds__(kSmallThreads, 2) combine_small_kernel(const C
       const bool live = q < pre[SB] && group_live(g, G, T);
       const int row = ((g + s) * slices + c) * 128 + i;  // < (65535 + 1024) * 4 * 128
       sq[u] = s;
-      ml[u] = live ? partial_state(a.ml_part[row]) : make_float2(-INFINITY, 0.f);
+      ml[u] = live ? a.ml_part[row] : make_float2(-INFINITY, 0.f);
       o[u] = live ? a.o_part[static_cast<long long>(row) * 128 + j] : 0.f;
     }
 #pragma unroll
     for (int u = 0; u < kSmallLoads; ++u) {
+      ml[u] = partial_state(ml[u]);
       if (ml[u].x == -INFINITY) continue;
 #pragma unroll
       for (int s = 0; s < SB; ++s) {
