@@ -41,18 +41,8 @@ constexpr int kPlanMinThreads = 128;
 constexpr int kPlanMaxBlocks = 128;
 constexpr int kPlanCluster = 8;
 
-// The sequence that owns item i of an exclusive prefix over B sequences (prefix[B] > i).
-__device__ __forceinline__ int owner(const int* prefix, int B, int i) {
-  int lo = 0, hi = B - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (prefix[mid + 1] > i) hi = mid; else lo = mid + 1;
-  }
-  return lo;
-}
-
 // Every block reads all lengths and scans them (one thread for a sequence), and takes its
-// share of the pages and tokens; block 0 writes what there is one of for a sequence.  With
+// share of the pages and tokens (whose sequence is found in the prefix sums, as a tile's is); block 0 writes what there is one of for a sequence.  With
 // CLUSTER the blocks are one cluster and meet before those writes: the outputs may then be
 // the inputs' own buffers.
 template <bool CLUSTER>
@@ -177,20 +167,20 @@ __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) 
   if (ok) {
     // pages taken: the ring's next ones, in the order of the sequences
     for (int i = me; i < need_total; i += threads) {
-      const int s = owner(take_s, B, i);
+      const int s = seq_of_tile(take_s, B, i);
       a.block_table[static_cast<long long>(s) * a.max_pages + have_s[s] + (i - take_s[s])] = a.free_pages[place(head0, i)];
     }
     // pages given back: behind the ring's tail.  The ring holds every page at most once, so
     // these places are not among the ones read above.
     for (int i = me; i < freed_total; i += threads) {
-      const int s = owner(give_s, B, i);
+      const int s = seq_of_tile(give_s, B, i);
       a.free_pages[place(tail0, i)] = a.block_table[static_cast<long long>(s) * a.max_pages + (i - give_s[s])];
     }
   }
   for (int i = me; i < a.max_tokens; i += threads) {
     int slot = -1, pos = -1;
     if (i < n_tokens) {
-      const int s = owner(start_s, B, i);
+      const int s = seq_of_tile(start_s, B, i);
       pos = len_s[s] + (i - start_s[s]);
       const int p = pos / P;
       // a cached page from the table, a new one from the ring
