@@ -38,13 +38,15 @@
 //              that PV(i) reads without a wait.
 // Every wait is bounded, as in decode_split_sm100.cu.
 //
-// What bounds it: a 96-token tile takes 1860 cycles, half of a stream's loop of P.V and QK (1310 to
-// the scores), maximum (480), exponentials (1060), P (150) and the way to the next issue
+// What bounds it: a 96-token tile takes 1740 to 1910 cycles in a long loop, half of a stream's P.V and
+// QK (1310 to the scores), maximum (480), exponentials (1060), P (150) and the way to the next issue
 // (340); the tensor core is busy 46 % of the time, shared memory 55 to 70 % (160 KB a tile), and an
-// operation on it takes 150 to 200 cycles under that load.  64 x 32 k tokens, int8, h = 128: 640 us at
-// 1.9 GHz (2.2 TB/s of cache, 0.92 PFLOP/s), 760 under the power cap; the row-scaled kernel
-// takes 1096 for the same tokens.  128-token tiles or three groups on one O were equal or slower: they
-// must hand M from tile to tile.
+// operation on it takes 150 to 200 cycles under that load.  64 x 32 k tokens, int8, h = 128: 592 tiles
+// a CTA in 1.107 M cycles, 17 k of them before the first scores, 4 to 6 k at the end of each of
+// three segments; 660 us (a mean of 1.68 GHz; 2.0 TB/s of cache, 0.89 PFLOP/s), some 760 under steady
+// load, where the board's power cap sets the clock; the row-scaled kernel takes 1096 for the same
+// tokens.  128-token tiles or three groups on one O were equal or slower: they must hand M from tile to
+// tile.
 #include <cstdint>
 
 #include "decode_sm100.h"
@@ -653,7 +655,8 @@ decode_block_kernel(const __grid_constant__ CUtensorMap map_ckv, const __grid_co
         const long long slot = static_cast<long long>(g) + s;
         const long long at = (slot * gridDim.x + slice) * 128 + row;
         // Eight lanes exchange their rows' 16-byte pieces, so that a store covers whole 128-byte lines: with
-        // a lane for a row, 32 lines to an instruction, a segment's end took 6000 cycles, so 3500.
+        // a lane for a row, 32 lines to an instruction, a segment's end took 2500 cycles more (now 3600 to
+        // 6400 with the waits for the last P.V).
         const int group_row = row - (lane & 7);
         float4* dst = reinterpret_cast<float4*>(a.o_part + (at - (lane & 7)) * 128 + 64 * b) + (lane & 7);
 #pragma unroll 1

@@ -6,13 +6,14 @@
 //   the step.  One request per thread; exclusive prefix sums of the tokens, of the pages
 //   taken and of the pages given back place everything.  A few kilobytes are read and
 //   written: latency bounds it, so it is one launch, each block scanning all lengths itself
-//   (3.3 us for 64 requests, 6.4 us for 1024 with 65536 tokens).
+//   (3.4 us for 64 requests, 6.2 us for 1024 with 65536 tokens).
 // append: a cache row is the token's latent in the cache's format and its RoPE key turned
 //   by the token's position.  With one scale per block of tokens and 128-wide latent head,
 //   s = max|x| / top over the block; a block that grows token by token keeps the larger of
 //   its old scale and the new tokens', and the rows it already holds are brought to it.
-//   2 (d_c + 64) bytes a token in, d_c + 128 of cache and 2 (d_c + 64) of rows out: 5.5 us for 6.8 k
-//   tokens of 512 columns (3.0 us of HBM time), 2.8 us for a step of 64 tokens.
+//   2 (d_c + 64) bytes a token in, d_c + 128 of cache and 2 (d_c + 64) of rows out: 5.6 us for 6.8 k
+//   tokens of 512 columns (3.0 us of HBM time), 2.9 us for a step of 64 tokens.  The same 6.8 k tokens
+//   as bf16 take 4.0 us, with a scale per row (a run each, a warp's work) 21 us.
 // load: rows c * s and RoPE keys back as bf16, the form prefill reads.  HBM bounds it: 53 us for
 //   160 k rows of 512 columns, 87 % of the rate of a plain copy.
 #include <climits>
@@ -42,9 +43,9 @@ constexpr int kPlanMaxBlocks = 128;
 constexpr int kPlanCluster = 8;
 
 // Every block reads all lengths and scans them (one thread for a sequence), and takes its
-// share of the pages and tokens (whose sequence is found in the prefix sums, as a tile's is); block 0 writes what there is one of for a sequence.  With
-// CLUSTER the blocks are one cluster and meet before those writes: the outputs may then be
-// the inputs' own buffers.
+// share of the pages and tokens (whose sequence is found in the prefix sums, as a tile's is);
+// block 0 writes what there is one of for a sequence.  With CLUSTER the blocks are one cluster and
+// meet before those writes: the outputs may then be the inputs' own buffers.
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kMaxBatch) page_plan_kernel(const PlanArgs a) {
   __shared__ unsigned long long sum_pages[32], sum_tokens[32];
@@ -536,8 +537,9 @@ __global__ void __launch_bounds__(kLoadThreads) cache_load_kernel(const LoadArgs
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t stream) {
   // A thread for a sequence, and a token or so for a thread: a step of 64 requests is one block of
-  // 128, and 65536 tokens are spread over 64 SMs (11.8 us on one cluster's 8, 6.4 so).
-  // Blocks that read lengths which another block overwrites must meet, in one cluster.
+  // 128, and 65536 tokens are spread over 64 SMs.  Blocks that read lengths which another block
+  // overwrites must meet, in one cluster of 8: 13.4 us for 1024 requests and 65536 tokens in place, 6.0 in
+  // buffers of their own.
   const int threads = (a.batch > kPlanMinThreads ? a.batch + 31 : kPlanMinThreads) / 32 * 32;
   const int blocks = (a.max_tokens + threads - 1) / threads;
   const bool in_place = a.seq_lens == a.seq_lens_out || a.free_range == a.free_range_out;
