@@ -285,9 +285,10 @@ HRA_API hra_status hra_check_prefill_status(const hra_prefill_params* p, void* s
  * left as it was).
  * A step that cannot be served is refused as a whole: lengths and pool stay as they were, no
  * page is taken or given back, every slot is -1, and status says why (hra_check_plan_status
- * reads it).  A cached page that is none of the pool leaves its tokens without a slot (-1), and is given
- * back unseen when its request ends: the step that would take it from the ring is refused.  Slots and positions behind the last token are -1, so a captured step can be
- * replayed with any number of tokens up to max_tokens.
+ * reads it).  A cached page that is none of the pool leaves its tokens without a slot (-1), and
+ * is given back unseen when its request ends: the step that would take it from the ring is refused.
+ * Slots and positions behind the last token are -1, so a captured step can be replayed with any
+ * number of tokens up to max_tokens.
  * seq_lens_out and free_range_out may be seq_lens and free_range themselves; no other buffers may
  * overlap.  With buffers of their own, the same call can be made again and gives the same plan, and
  * plans of many tokens are faster (1024 requests, 65536 tokens: 6.0 us, in place 13.4).
